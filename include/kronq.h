@@ -505,6 +505,100 @@ kq_status kq_reverted_matvec(const uint32_t* packed, int64_t d_out, int64_t d_in
                              const float* X, int64_t ldx, int batch, float* Y, int64_t ldy,
                              void* ws, size_t ws_bytes, kq_stream_t stream);
 
+/* --------------------------------------------------------------------------
+ * Microscaled 4-bit floating point: a hardware number format for the same
+ * linears, next to the integer grids above.
+ *
+ * A matrix [rows, cols] is held as e2m1 codes (sign bit, magnitudes 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6), two per byte, the even column in the low nibble, rows of
+ * `ld` bytes; and one scale per block of a row:
+ *   KQ_FP4_MX  32 columns, E8M0 byte b = 2^(b - 127) (0xFF NaN)
+ *              (OCP Microscaling Formats specification, MXFP4);
+ *   KQ_FP4_NV  16 columns, E4M3 byte s; the block's scale is s * gscale.
+ * Codes past `cols`, up to a multiple of 32 columns, are zero.  Scale bytes lie
+ * in tiles of 128 rows x 4 blocks (the tensor core's layout): row r, block b at
+ *   ((r / 128) * ceil(blocks / 4) + b / 4) * 512 + (r % 32) * 16
+ *     + (r % 128) / 32 * 4 + b % 4,
+ * kq_fp4_scale_bytes(rows, cols, format) bytes in all, the places of rows and
+ * blocks that do not exist zero.
+ *
+ *   kq_fp4     rows >= 0 (at most 2^30), 1 <= cols <= 2^24; codes and scales
+ *              16-byte aligned, ld % 16 == 0, ld >= ceil(cols / 32) * 16;
+ *              gscale: device fp32[1], KQ_FP4_NV only (NULL there: 1), NULL for
+ *              KQ_FP4_MX.  The struct is host memory, read during the call.
+ *
+ * kq_fp4_quantize: M [Q->rows, Q->cols] (dtype KQ_F32 or KQ_BF16, ldm >= cols,
+ *   aligned to its elements) to Q's codes and scales, padding included.
+ *   MX: scale 2^k, k = floor(log2(amax)) - 2 in -127..127 (a block of zeros:
+ *   byte 0).  NV (gscale required): s = E4M3 nearest to fl(amax / fl(6 g)), at
+ *   most 448.  Codes: v / d rounded to nearest even and saturated at 6, d the
+ *   fp32 scale, the quotient rounded to fp32 (0 where d is 0).  M_hat (may be
+ *   NULL): the fp32 values the codes stand for, ldh >= cols.  A block that holds
+ *   NaN or Inf gets the NaN scale and codes 0 and is reported in `info`
+ *   (KQ_ERR_NONFINITE, index = row); so does every block when gscale is not
+ *   positive and finite (KQ_ERR_INVALID_ARG).  M_hat must not overlap M.
+ * kq_fp4_gemm: Y [A->rows, B->rows] = A B^T (same format and columns), dtype
+ *   KQ_F32 or KQ_BF16, ldy >= B->rows.  Block-scaled tensor-core products,
+ *   fp32 sums.  Any number of rows from 0; `info`: KQ_ERR_TIMEOUT.
+ * kq_fp4_matvec: Y[b, :] = W X[b, :] for b < batch (1..8) with unquantised
+ *   vectors, the single-token form of the product: X [batch, W->cols] and Y
+ *   [batch, W->rows] both of `dtype` (KQ_F32 or KQ_BF16), fp32 sums.
+ * kq_fp4_gated_ffn: H [X->rows, f] = act(X W_gate^T) * (X W_up^T), bf16, over
+ *   4-bit X [T, d] and weights [f, d] of one format: both projections, the
+ *   activation and the product in one kernel (see kq_gated_ffn).
+ * ------------------------------------------------------------------------ */
+enum { KQ_F32 = 0, KQ_BF16 = 1 };
+enum { KQ_FP4_MX = 0, KQ_FP4_NV = 1 };
+enum { KQ_ACT_SILU = 0, KQ_ACT_GELU = 1 };
+
+typedef struct kq_fp4 {
+  int64_t rows, cols, ld;
+  int32_t format;
+  uint8_t* codes;
+  uint8_t* scales;
+  const float* gscale;
+} kq_fp4;
+
+size_t kq_fp4_scale_bytes(int64_t rows, int64_t cols, int format);
+kq_status kq_fp4_quantize(const void* M, int dtype, int64_t ldm, const kq_fp4* Q, float* M_hat, int64_t ldh,
+                          int32_t* info, kq_stream_t stream);
+kq_status kq_fp4_gemm(const kq_fp4* A, const kq_fp4* B, void* Y, int dtype, int64_t ldy, int32_t* info,
+                      kq_stream_t stream);
+kq_status kq_fp4_matvec(const kq_fp4* W, const void* X, int dtype, int64_t ldx, int batch, void* Y, int64_t ldy,
+                        kq_stream_t stream);
+kq_status kq_fp4_gated_ffn(const kq_fp4* X, const kq_fp4* W_gate, const kq_fp4* W_up, int act, uint16_t* H,
+                           int64_t ldh, int32_t* info, kq_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * kq_gated_ffn - the gated half of an MLP in bf16, and its backward pass.
+ *
+ * H = act(X W_gate^T) * (X W_up^T) for X [tokens, d] and weights [f, d]; act is
+ * KQ_ACT_SILU (g sigmoid(g)) or KQ_ACT_GELU (tanh form).  Both projections, the
+ * activation and the product in one kernel, fp32 until H is rounded.
+ *
+ * kq_gated_ffn_backward: from dH [tokens, f], with G and U formed again in
+ *   fp32:  dU = dH act(G), dG = dH U act'(G) (bf16 outputs, [tokens, f]);
+ *   dX [tokens, d] = dG W_gate + dU W_up;  dW_gate = dG^T X, dW_up = dU^T X
+ *   ([f, d]), the products taking dG and dU as rounded to bf16.  dG and dU are
+ *   the output gradients of the gate and up linears and H (written too when not
+ *   NULL) the input of the down linear: the A matrices of kq_accum_cov.  dX and
+ *   the pair dW_gate, dW_up may be NULL (not computed).
+ *   X, weights, dG, dU: 16-byte aligned, leading dimensions % 8 == 0; the other
+ *   tensors aligned to their elements.  No output may overlap an input or
+ *   another output.  tokens == 0: the weights' gradients are zeros, the other
+ *   tensors may be NULL.
+ * All bf16 as uint16_t bit patterns.  Limits: 0 <= tokens <= 2^24, 1 <= d, f <=
+ * 2^20.  `info`: KQ_ERR_TIMEOUT.  NaN and Inf propagate.
+ * ------------------------------------------------------------------------ */
+kq_status kq_gated_ffn(const uint16_t* X, int64_t tokens, int64_t d, int64_t ldx, const uint16_t* W_gate,
+                       const uint16_t* W_up, int64_t f, int64_t ldw, int act, uint16_t* H, int64_t ldh,
+                       int32_t* info, kq_stream_t stream);
+kq_status kq_gated_ffn_backward(const uint16_t* X, int64_t tokens, int64_t d, int64_t ldx, const uint16_t* W_gate,
+                                const uint16_t* W_up, int64_t f, int64_t ldw, int act, const uint16_t* dH,
+                                int64_t lddh, uint16_t* dG, uint16_t* dU, int64_t ldg, uint16_t* H, int64_t ldh,
+                                uint16_t* dX, int64_t lddx, uint16_t* dW_gate, uint16_t* dW_up, int64_t lddw,
+                                int32_t* info, kq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

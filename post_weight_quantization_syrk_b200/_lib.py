@@ -24,6 +24,9 @@ STATUS_NAMES = {
 }
 KQ_AXIS_ROWS, KQ_AXIS_COLS = 0, 1
 KQ_GEMM_FP32, KQ_GEMM_3XTF32 = 0, 1
+KQ_F32, KQ_BF16 = 0, 1
+KQ_FP4_MX, KQ_FP4_NV = 0, 1
+KQ_ACT_SILU, KQ_ACT_GELU = 0, 1
 
 # Every symbol the header declares.
 EXPORTS = (
@@ -40,6 +43,8 @@ EXPORTS = (
     "kq_kron_loss_workspace_size", "kq_kron_loss", "kq_kron_loss_multi", "kq_kron_loss_noalloc",
     "kq_kron_loss_blocks_workspace_size", "kq_kron_loss_blocks",
     "kq_allocate_bits",
+    "kq_fp4_scale_bytes", "kq_fp4_quantize", "kq_fp4_gemm", "kq_fp4_matvec", "kq_fp4_gated_ffn",
+    "kq_gated_ffn", "kq_gated_ffn_backward",
 )
 
 
@@ -55,6 +60,11 @@ class kq_solver_times(ctypes.Structure):
                 ("grid_launches", ctypes.c_longlong), ("inblock_launches", ctypes.c_longlong),
                 ("update_launches", ctypes.c_longlong), ("update_flops", ctypes.c_double),
                 ("inblock_bytes", ctypes.c_double)]
+
+
+class kq_fp4(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("format", ctypes.c_int32),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("gscale", ctypes.c_void_p)]
 
 
 class kq_rht(ctypes.Structure):
@@ -105,6 +115,15 @@ _SIGS = {
     "kq_reverted_matvec_workspace_size": (_sz, [_i64, _i32]),
     "kq_reverted_matvec": (_i32, [_vp, _i64, _i64, _i64, _i32, _vp, _vp, _i32, ctypes.POINTER(kq_rht),
                                   ctypes.POINTER(kq_rht), _vp, _i64, _i32, _vp, _i64, _vp, _sz, _vp]),
+    "kq_fp4_scale_bytes": (_sz, [_i64, _i64, _i32]),
+    "kq_fp4_quantize": (_i32, [_vp, _i32, _i64, ctypes.POINTER(kq_fp4), _vp, _i64, _vp, _vp]),
+    "kq_fp4_gemm": (_i32, [ctypes.POINTER(kq_fp4), ctypes.POINTER(kq_fp4), _vp, _i32, _i64, _vp, _vp]),
+    "kq_fp4_matvec": (_i32, [ctypes.POINTER(kq_fp4), _vp, _i32, _i64, _i32, _vp, _i64, _vp]),
+    "kq_fp4_gated_ffn": (_i32, [ctypes.POINTER(kq_fp4), ctypes.POINTER(kq_fp4), ctypes.POINTER(kq_fp4), _i32, _vp, _i64,
+                                _vp, _vp]),
+    "kq_gated_ffn": (_i32, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _i32, _vp, _i64, _vp, _vp]),
+    "kq_gated_ffn_backward": (_i32, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _i64, _vp,
+                                     _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp]),
     "kq_allocate_bits": (_i32, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64), _i32,
                                 ctypes.POINTER(ctypes.c_int), _i32, _f64, ctypes.POINTER(ctypes.c_int)]),
 }
@@ -546,3 +565,203 @@ def kq_solver_timing(enable):
     if enable:
         return None
     return {f: getattr(t, f) for f, _ in kq_solver_times._fields_}
+
+
+# ------------------------------------- microscaled 4-bit floating point
+
+_DTYPES = {torch.float32: KQ_F32, torch.bfloat16: KQ_BF16}
+
+
+def _on_device(*tensors):
+    """The tensors lie on one CUDA device, the current one (whose stream the work goes to)."""
+    dev = tensors[0].device
+    if not tensors[0].is_cuda or dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors must lie on the current CUDA device, got {dev}")
+    for t in tensors[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors must lie on one device")
+
+
+def _dtype_code(t, name):
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _out(t, shape, dtype, device, name, multiple=1):
+    """An output matrix and its leading dimension: checked, or a new one whose
+    rows lie a multiple of `multiple` elements apart."""
+    if t is None:
+        rows, cols = shape
+        ld = -(-cols // multiple) * multiple
+        t = torch.empty((rows, ld), dtype=dtype, device=device)
+        return (t if ld == cols else t[:, :cols]), ld
+    ld = _mat(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}")
+    return t, ld
+
+
+class Fp4Matrix:
+    """A microscaled 4-bit matrix (layout in kronq.h): codes uint8 [rows, >= ceil(cols / 32) * 16],
+    tiled scales uint8, and for KQ_FP4_NV the global scale (float32, one element)."""
+
+    def __init__(self, rows, cols, format, codes, scales, gscale=None):
+        rows, cols, format = int(rows), int(cols), int(format)
+        if format not in (KQ_FP4_MX, KQ_FP4_NV):
+            raise ValueError("format must be KQ_FP4_MX or KQ_FP4_NV")
+        ld = _mat(codes, torch.uint8, "codes")
+        if codes.shape[0] != rows or codes.shape[1] < -(-cols // 32) * 16:
+            raise ValueError("codes must be [rows, >= ceil(cols / 32) * 16]")
+        if codes.shape[0] <= 1:
+            ld = -(-ld // 16) * 16      # a single row: the distance to the next is not used
+        if scales.dtype != torch.uint8 or not scales.is_contiguous() or \
+                scales.numel() < kq_fp4_scale_bytes(rows, cols, format):
+            raise ValueError("scales must be contiguous uint8 with kq_fp4_scale_bytes(rows, cols, format) elements")
+        if gscale is not None and (gscale.dtype != torch.float32 or gscale.numel() != 1):
+            raise TypeError("gscale must be one float32 element")
+        for t in (scales, gscale):
+            if t is not None and t.device != codes.device:
+                raise ValueError("codes, scales and gscale must lie on one device")
+        self.rows, self.cols, self.format = rows, cols, format
+        self.codes, self.scales, self.gscale = codes, scales, gscale
+        self.device = codes.device
+        self.is_cuda = codes.is_cuda
+        self.c = kq_fp4(rows, cols, ld, format, codes.data_ptr(), scales.data_ptr(),
+                        0 if gscale is None else gscale.data_ptr())
+
+
+def kq_fp4_scale_bytes(rows: int, cols: int, format: int) -> int:
+    return int(load().kq_fp4_scale_bytes(int(rows), int(cols), int(format)))
+
+
+def kq_fp4_quantize(M, format, gscale=None, M_hat=None, out=None, info=None, stream=None):
+    """M (float32 or bf16 [rows, cols]) to a microscaled 4-bit matrix; M_hat
+    float32 [rows, cols]: the values its codes stand for."""
+    dtype = _dtype_code(M, "M")
+    ldm = _mat(M, M.dtype, "M")
+    rows, cols = M.shape
+    _on_device(M, gscale, M_hat, info)
+    if out is None:
+        codes = torch.empty((rows, -(-cols // 32) * 16), dtype=torch.uint8, device=M.device)
+        scales = torch.empty(kq_fp4_scale_bytes(rows, cols, format), dtype=torch.uint8, device=M.device)
+        out = Fp4Matrix(rows, cols, format, codes, scales, gscale)
+    else:
+        _on_device(M, out)
+        if (out.rows, out.cols, out.format) != (rows, cols, int(format)):
+            raise ValueError("out has another shape or format")
+        if gscale is not None and (out.gscale is None or out.gscale.data_ptr() != gscale.data_ptr()):
+            raise ValueError("out has another gscale")
+    ldh = cols if M_hat is None else _out(M_hat, (rows, cols), torch.float32, M.device, "M_hat")[1]
+    if info is None:
+        info = new_info(M.device)
+    _check(load().kq_fp4_quantize(M.data_ptr(), dtype, ldm, out.c, None if M_hat is None else M_hat.data_ptr(), ldh,
+                                  info.data_ptr(), _stream(stream)), "kq_fp4_quantize")
+    return out
+
+
+def kq_fp4_gemm(A, B, Y=None, dtype=torch.bfloat16, info=None, stream=None):
+    """Y [A.rows, B.rows] = A B^T, bf16 or float32."""
+    if Y is not None:
+        dtype = Y.dtype
+    if dtype not in _DTYPES:
+        raise TypeError("Y must be float32 or bfloat16")
+    _on_device(A, B, Y, info)
+    Y, ldy = _out(Y, (A.rows, B.rows), dtype, A.device, "Y", 8)
+    if info is None:
+        info = new_info(A.device)
+    _check(load().kq_fp4_gemm(A.c, B.c, Y.data_ptr(), _DTYPES[dtype], ldy, info.data_ptr(), _stream(stream)),
+           "kq_fp4_gemm")
+    return Y
+
+
+def kq_fp4_matvec(W, X, Y=None, stream=None):
+    """Y [batch, W.rows] = X W^T for unquantized X [batch (1..8), W.cols], in X's dtype."""
+    dtype = _dtype_code(X, "X")
+    ldx = _mat(X, X.dtype, "X")
+    _on_device(W, X, Y)
+    batch = X.shape[0]
+    if X.shape[1] != W.cols:
+        raise ValueError("X must be [batch, W.cols]")
+    Y, ldy = _out(Y, (batch, W.rows), X.dtype, X.device, "Y")
+    _check(load().kq_fp4_matvec(W.c, X.data_ptr(), dtype, ldx, batch, Y.data_ptr(), ldy, _stream(stream)),
+           "kq_fp4_matvec")
+    return Y
+
+
+def kq_fp4_gated_ffn(X, W_gate, W_up, act, H=None, info=None, stream=None):
+    """H [X.rows, f] bf16 = act(X W_gate^T) * (X W_up^T) over 4-bit X and weights [f, d]."""
+    _on_device(X, W_gate, W_up, H, info)
+    H, ldh = _out(H, (X.rows, W_gate.rows), torch.bfloat16, X.device, "H", 8)
+    if info is None:
+        info = new_info(X.device)
+    _check(load().kq_fp4_gated_ffn(X.c, W_gate.c, W_up.c, int(act), H.data_ptr(), ldh, info.data_ptr(),
+                                   _stream(stream)), "kq_fp4_gated_ffn")
+    return H
+
+
+# ------------------------------------- gated feed-forward block, bf16
+
+def _tma_mat(t, name):
+    """Leading dimension of a bf16 matrix that a kernel reads by TMA."""
+    ld = _mat(t, torch.bfloat16, name)
+    return -(-ld // 8) * 8 if t.shape[0] <= 1 else ld     # a single row: the distance to the next is not used
+
+
+def _gated_weights(X, W_gate, W_up):
+    ldw = _tma_mat(W_gate, "W_gate")
+    if W_up.shape != W_gate.shape or _tma_mat(W_up, "W_up") != ldw:
+        raise ValueError("W_gate and W_up need the same shape and leading dimension")
+    if W_gate.shape[1] != X.shape[1]:
+        raise ValueError("X [tokens, d], weights [f, d]")
+    return ldw
+
+
+def kq_gated_ffn(X, W_gate, W_up, act, H=None, info=None, stream=None):
+    """H [tokens, f] = act(X W_gate^T) * (X W_up^T), all bf16."""
+    ldx, ldw = _tma_mat(X, "X"), _gated_weights(X, W_gate, W_up)
+    _on_device(X, W_gate, W_up, H, info)
+    (tokens, d), f = X.shape, W_gate.shape[0]
+    H, ldh = _out(H, (tokens, f), torch.bfloat16, X.device, "H", 8)
+    if info is None:
+        info = new_info(X.device)
+    _check(load().kq_gated_ffn(X.data_ptr(), tokens, d, ldx, W_gate.data_ptr(), W_up.data_ptr(), f, ldw, int(act),
+                               H.data_ptr(), ldh, info.data_ptr(), _stream(stream)), "kq_gated_ffn")
+    return H
+
+
+def kq_gated_ffn_backward(X, W_gate, W_up, dH, act, dG=None, dU=None, H=None, dX=None, dW_gate=None, dW_up=None,
+                          need_dX=True, need_dW=True, info=None, stream=None):
+    """(dG, dU, dX, dW_gate, dW_up) of kq_gated_ffn, all bf16; H (when given)
+    gets the block's output.  need_dX / need_dW False: None in those places."""
+    ldx, ldw = _tma_mat(X, "X"), _gated_weights(X, W_gate, W_up)
+    lddh = _mat(dH, torch.bfloat16, "dH")
+    _on_device(X, W_gate, W_up, dH, dG, dU, H, dX, dW_gate, dW_up, info)
+    (tokens, d), f = X.shape, W_gate.shape[0]
+    if tuple(dH.shape) != (tokens, f):
+        raise ValueError("dH must be [tokens, f]")
+    bf, dev = torch.bfloat16, X.device
+    dG, ldg = _out(dG, (tokens, f), bf, dev, "dG", 8)
+    dU, ldu = _out(dU, (tokens, f), bf, dev, "dU", 8)
+    if tokens <= 1:
+        ldg = ldu = -(-max(ldg, ldu) // 8) * 8
+    if ldg != ldu:
+        raise ValueError("dG and dU need the same leading dimension")
+    ldh = f if H is None else _out(H, (tokens, f), bf, dev, "H")[1]
+    lddx = lddw = d
+    if need_dX:
+        dX, lddx = _out(dX, (tokens, d), bf, dev, "dX", 8)
+    if need_dW:
+        dW_gate, lddw = _out(dW_gate, (f, d), bf, dev, "dW_gate", 8)
+        dW_up, ld2 = _out(dW_up, (f, d), bf, dev, "dW_up", 8)
+        if ld2 != lddw:
+            raise ValueError("dW_gate and dW_up need the same leading dimension")
+    if info is None:
+        info = new_info(dev)
+    _check(load().kq_gated_ffn_backward(
+        X.data_ptr(), tokens, d, ldx, W_gate.data_ptr(), W_up.data_ptr(), f, ldw, int(act), dH.data_ptr(), lddh,
+        dG.data_ptr(), dU.data_ptr(), ldg, None if H is None else H.data_ptr(), ldh,
+        dX.data_ptr() if need_dX else None, lddx, dW_gate.data_ptr() if need_dW else None,
+        dW_up.data_ptr() if need_dW else None, lddw, info.data_ptr(), _stream(stream)), "kq_gated_ffn_backward")
+    return dG, dU, (dX if need_dX else None), (dW_gate if need_dW else None), (dW_up if need_dW else None)

@@ -1,0 +1,490 @@
+// Microscaled 4-bit floating point: quantization to e2m1 codes with block
+// scales (kq_fp4_quantize), and the matvec of such a matrix with up to eight
+// unquantized vectors (kq_fp4_matvec), the single-token form of the product.
+//
+// Formats (OCP Microscaling Formats specification, MXFP4; and the two-level
+// form with E4M3 scales): a block of 32 columns shares one E8M0 scale
+// 2^(floor(log2 amax) - 2), or a block of 16 shares the scale s g, s the E4M3
+// value nearest to amax / (6 g) and g one fp32 number per matrix.
+#include <cuda_bf16.h>
+
+#include "kq_fp4.cuh"
+
+namespace {
+
+using kq::fp4::block_of;
+
+// ------------------------------------------------------------------ quantize
+
+template <typename T>
+__device__ __forceinline__ float as_float(T v);
+template <>
+__device__ __forceinline__ float as_float<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Eight elements from column c of a row, zeros past `cols`.
+__device__ __forceinline__ void load8(const float* row, int64_t c, int64_t cols, bool vec, float (&v)[8]) {
+  if (vec && c + 8 <= cols) {
+    const float4 a = *reinterpret_cast<const float4*>(row + c), b = *reinterpret_cast<const float4*>(row + c + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? row[c + i] : 0.f;
+  }
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* row, int64_t c, int64_t cols, bool vec, float (&v)[8]) {
+  if (vec && c + 8 <= cols) {
+    const uint4 q = *reinterpret_cast<const uint4*>(row + c);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? __bfloat162float(row[c + i]) : 0.f;
+  }
+}
+
+// Eight values to eight codes: round to nearest even, saturating at 6.
+__device__ __forceinline__ uint32_t encode8(const float (&q)[8]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+  return w;
+}
+
+// The value of code k of a word.
+__device__ __forceinline__ float decode1(uint32_t w, int k) {
+  const uint32_t c = (w >> (4 * k)) & 15u, m = c & 7u;
+  // e2m1 as the top bits of an fp32 with exponent bias 127 - 126: exact, subnormal included
+  const float v = __uint_as_float(m << 22) * 0x1p126f;
+  return c & 8u ? -v : v;
+}
+
+struct QuantParams {
+  int64_t rows, cols, ldm, ldc, ldh;
+  int64_t chunks;       // 256-column pieces of a row, the scale tiles' padding included
+  int64_t units;        // (rows rounded up to 128) / R * chunks
+  int64_t kat;          // scale tiles along a row
+  const void* M;
+  const float* g;
+  uint8_t* codes;
+  uint8_t* scales;
+  float* M_hat;
+  int m_vec, h_vec;
+  int32_t* info;
+};
+
+// One warp per 256 columns of R rows, eight columns per lane (so a lane's loads,
+// its 4 bytes of codes and its dequantized values are contiguous across the
+// warp); the R rows' loads are in flight together.  A block is 4 lanes (32
+// columns) or 2 (16): its amax is 2 or 1 shuffles away, and every fourth block's
+// lanes write 4 scale bytes as one word.  Bound by memory: one read of M, one
+// write of codes and scales (and of M_hat).
+template <typename T, int FMT, int R>
+__global__ void __launch_bounds__(256) quantize_kernel(const QuantParams p) {
+  constexpr int LANES = block_of(FMT) / 8;        // lanes per block
+  const int lane = threadIdx.x % 32;
+  float g = 1.f, g6 = 6.f;
+  bool g_ok = true;
+  if (FMT == KQ_FP4_NV) {
+    g = *p.g;
+    g_ok = g > 0.f && isfinite(g);
+    g6 = 6.f * g;
+  }
+  const int64_t padded = (p.cols + 31) / 32 * 32;
+  for (int64_t unit = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; unit < p.units; unit += (int64_t)gridDim.x * 8) {
+    const int64_t r0 = unit / p.chunks * R, c = unit % p.chunks * 256 + 8 * lane;
+    float v[R][8];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (r0 + k < p.rows && c < p.cols) {
+        load8(static_cast<const T*>(p.M) + (r0 + k) * p.ldm, c, p.cols, p.m_vec, v[k]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int64_t r = r0 + k;
+      // amax as bits: non-negative floats order as integers, and NaN and Inf lie on top
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[k][i]) & 0x7fffffffu);
+#pragma unroll
+      for (int o = 1; o < LANES; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float amax = __uint_as_float(top);
+      const bool bad = top >= 0x7f800000u || !g_ok;
+      uint32_t byte;
+      float d, q[8];
+      if (FMT == KQ_FP4_MX) {
+        // 2^(floor(log2 amax) - 2) from the exponent field; at least 2^-127
+        const int field = max((int)(top >> 23) - 2, 0);
+        byte = bad ? 0xffu : (uint32_t)field;
+        d = field ? __uint_as_float((uint32_t)field << 23) : 0x1p-127f;
+        const float inv = __uint_as_float((uint32_t)(254 - field) << 23);   // 1 / d, a power of two
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = v[k][i] * inv;
+      } else {
+        const float t = fminf(__fdiv_rn(amax, g6), 448.f);
+        uint16_t pair;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pair) : "f"(0.f), "f"(t));
+        byte = bad ? 0x7fu : (uint32_t)(pair & 0xff);
+        d = kq::fp4::e4m3_value(byte) * g;
+        // v / d rounded to fp32.  With the reciprocal r rounded once per block,
+        // q0 = v r is within 2 ulp and fma(v - q0 d, r, q0) is the rounded
+        // quotient (Markstein's correction step: the residual is exact in an
+        // fma); a divide per element would bound the kernel.  Outside the
+        // range where the residual is exact, the divide.
+        if (d >= 0x1p-90f && d <= 0x1p90f && amax <= 1024.f * d) {
+          const float r = __frcp_rn(d);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float q0 = v[k][i] * r;
+            q[i] = fmaf(fmaf(-q0, d, v[k][i]), r, q0);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) q[i] = d > 0.f ? __fdiv_rn(v[k][i], d) : 0.f;
+        }
+      }
+      uint32_t w = bad ? 0u : encode8(q);
+      if (bad && r < p.rows && c < p.cols) kq::report(p.info, g_ok ? KQ_ERR_NONFINITE : KQ_ERR_INVALID_ARG, r);
+      if (r < p.rows && c < padded) *reinterpret_cast<uint32_t*>(p.codes + r * p.ldc + c / 2) = w;
+      // four blocks' bytes as one word, written by the first lane of the four
+      uint32_t word = byte << (8 * ((lane / LANES) & 3));
+#pragma unroll
+      for (int o = LANES; o < 4 * LANES; o *= 2) word |= __shfl_xor_sync(0xffffffffu, word, o);
+      const int64_t kb = c / block_of(FMT);
+      // a block past the row's end is a block of zeros: byte 0
+      if (lane % (4 * LANES) == 0 && kb / 4 < p.kat)
+        *reinterpret_cast<uint32_t*>(p.scales + kq::fp4::scale_offset(r, kb, p.kat)) = r < p.rows ? word : 0u;
+      if (p.M_hat && r < p.rows && c < p.cols) {
+        if (bad) d = __uint_as_float(0x7fc00000u);
+        float* dst = p.M_hat + r * p.ldh + c;
+        float h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = decode1(w, i) * d;
+        if (p.h_vec && c + 8 <= p.cols) {
+          reinterpret_cast<float4*>(dst)[0] = make_float4(h[0], h[1], h[2], h[3]);
+          reinterpret_cast<float4*>(dst)[1] = make_float4(h[4], h[5], h[6], h[7]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < p.cols) dst[i] = h[i];
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ matvec
+
+// Weights as the 16-row operand of mma.m16n8k16 (bf16, fp32 accumulation), the
+// vectors as its 8 columns, so that one decode of a code serves all vectors.
+// e2m1 times its scale has at most 6 significant bits: exact in bf16.  bf16
+// vectors enter as they are; fp32 vectors as three bf16 parts that sum to them
+// (24 bits), one MMA each.
+//
+// A warp takes 128 columns of 16 rows per step; lane (g, t) = (lane / 4, lane %
+// 4) holds 32 consecutive codes of rows g and g + 8 (16-byte loads).  The K
+// order inside an MMA is free as long as both operands share it: a register
+// pairs codes p and p + 4 of a word, which three logic operations bring to
+// bf16 position, and x is paired alike.  The warps of a CTA split K; their sums
+// are added in warp order through shared memory.
+constexpr int kWarps = 8;
+
+struct MatvecParams {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const float* g;
+  int64_t d_out, d_in, ldc, kat;
+  const void* X;
+  int64_t ldx;
+  int x_vec, batch;
+  void* Y;
+  int64_t ldy;
+};
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Codes p and p + 4 of a word as bf16 values times 2^-126.
+template <int P>
+__device__ __forceinline__ uint32_t spread(uint32_t w) {
+  const uint32_t mag = P < 2 ? w << (6 - 4 * P) : w >> (4 * P - 6);
+  const uint32_t sgn = w << (12 - 4 * P);
+  return (mag & 0x01c001c0u) | (sgn & 0x80008000u);
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// A block's scale as a bf16 pair to multiply spread() with: MX 2^k (after 2^126),
+// NV s 2^118 (the missing 2^8 is in the final factor; 448 2^126 would overflow).
+template <int FMT>
+__device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
+  uint32_t h;
+  if (FMT == KQ_FP4_MX) {
+    h = byte == 0xffu ? 0x7fc0u : (byte ? byte << 7 : 0x0040u);
+  } else {
+    const float s = kq::fp4::e4m3_value(byte) * 0x1p118f;
+    h = __float_as_uint(s) >> 16;
+  }
+  return h | (h << 16);
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t weight(uint32_t spread_pair, uint32_t scale) {
+  if (FMT == KQ_FP4_MX) spread_pair = mul_bf16x2(spread_pair, 0x7e807e80u);   // 2^126
+  return mul_bf16x2(spread_pair, scale);
+}
+
+// 32 elements of a vector as pairs (8 j + p, 8 j + p + 4), in `PARTS` bf16 parts.
+template <typename T, int PARTS>
+__device__ __forceinline__ void load_x(const T* x, int64_t k, int64_t d_in, bool ok, bool vec, uint32_t (&b)[PARTS][16]) {
+  if constexpr (PARTS == 1) {
+    uint32_t w[16];
+    if (ok && vec && k + 32 <= d_in) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 q = *reinterpret_cast<const uint4*>(x + k + 8 * i);
+        w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t lo = ok && k + 2 * i < d_in ? __bfloat16_as_ushort(x[k + 2 * i]) : 0u;
+        const uint32_t hi = ok && k + 2 * i + 1 < d_in ? __bfloat16_as_ushort(x[k + 2 * i + 1]) : 0u;
+        w[i] = lo | (hi << 16);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      b[0][4 * j] = __byte_perm(w[4 * j], w[4 * j + 2], 0x5410);
+      b[0][4 * j + 1] = __byte_perm(w[4 * j], w[4 * j + 2], 0x7632);
+      b[0][4 * j + 2] = __byte_perm(w[4 * j + 1], w[4 * j + 3], 0x5410);
+      b[0][4 * j + 3] = __byte_perm(w[4 * j + 1], w[4 * j + 3], 0x7632);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float v[8];
+      if (ok && vec && k + 8 * j + 8 <= d_in) {
+        const float4 q0 = *reinterpret_cast<const float4*>(x + k + 8 * j), q1 = *reinterpret_cast<const float4*>(x + k + 8 * j + 4);
+        v[0] = q0.x; v[1] = q0.y; v[2] = q0.z; v[3] = q0.w;
+        v[4] = q1.x; v[5] = q1.y; v[6] = q1.z; v[7] = q1.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = ok && k + 8 * j + i < d_in ? as_float(x[k + 8 * j + i]) : 0.f;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float lo = v[q], hi = v[q + 4];
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) {
+          const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+          b[part][4 * j + q] = *reinterpret_cast<const uint32_t*>(&r);
+          // the remainder is exact; an infinity (or a value that rounds to one) has none
+          lo = isfinite(__low2float(r)) ? lo - __low2float(r) : 0.f;
+          hi = isfinite(__high2float(r)) ? hi - __high2float(r) : 0.f;
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kWarps * 32) matvec_kernel(const MatvecParams p) {
+  constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
+  __shared__ float sums[kWarps][16][8];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int64_t r0 = (int64_t)blockIdx.x * 16;
+  const int64_t chunks = (p.d_in + 127) / 128, padded = (p.d_in + 31) / 32 * 32;
+  const T* x = static_cast<const T*>(p.X) + (g < p.batch ? g : 0) * p.ldx;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int64_t ch = warp; ch < chunks; ch += kWarps) {
+    const int64_t k = 128 * ch + 32 * t;
+    uint4 w[2];
+    uint32_t s[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t r = r0 + g + 8 * h;
+      w[h] = make_uint4(0, 0, 0, 0);
+      s[h] = 0;
+      if (r < p.d_out && k < padded) {
+        w[h] = *reinterpret_cast<const uint4*>(p.codes + r * p.ldc + k / 2);
+        if (FMT == KQ_FP4_MX)
+          s[h] = p.scales[kq::fp4::scale_offset(r, k / 32, p.kat)];
+        else
+          s[h] = *reinterpret_cast<const uint16_t*>(p.scales + kq::fp4::scale_offset(r, k / 16, p.kat));
+      }
+    }
+    uint32_t b[PARTS][16];
+    load_x<T, PARTS>(x, k, p.d_in, g < p.batch, p.x_vec, b);
+    uint32_t sc[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      sc[h][0] = scale_pair<FMT>(s[h] & 0xffu);
+      sc[h][1] = FMT == KQ_FP4_MX ? sc[h][0] : scale_pair<FMT>(s[h] >> 8);
+    }
+    // the tensor core truncates as it accumulates: one chain per 128 columns,
+    // the chains summed in rounded fp32
+    float part_acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const uint32_t w0[4] = {w[0].x, w[0].y, w[0].z, w[0].w}, w1[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t s0 = sc[0][j / 2], s1 = sc[1][j / 2];
+      const uint32_t a[8] = {weight<FMT>(spread<0>(w0[j]), s0), weight<FMT>(spread<0>(w1[j]), s1),
+                             weight<FMT>(spread<1>(w0[j]), s0), weight<FMT>(spread<1>(w1[j]), s1),
+                             weight<FMT>(spread<2>(w0[j]), s0), weight<FMT>(spread<2>(w1[j]), s1),
+                             weight<FMT>(spread<3>(w0[j]), s0), weight<FMT>(spread<3>(w1[j]), s1)};
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part) {
+        mma16816(part_acc, a[0], a[1], a[2], a[3], b[part][4 * j], b[part][4 * j + 1]);
+        mma16816(part_acc, a[4], a[5], a[6], a[7], b[part][4 * j + 2], b[part][4 * j + 3]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] += part_acc[i];
+  }
+  sums[warp][g][2 * t] = acc[0];
+  sums[warp][g][2 * t + 1] = acc[1];
+  sums[warp][g + 8][2 * t] = acc[2];
+  sums[warp][g + 8][2 * t + 1] = acc[3];
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    const int row = threadIdx.x % 16, n = threadIdx.x / 16;
+    const int64_t r = r0 + row;
+    if (n < p.batch && r < p.d_out) {
+      float v = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) v += sums[i][row][n];
+      if (FMT == KQ_FP4_NV) v *= 256.f * (p.g ? *p.g : 1.f);
+      if constexpr (sizeof(T) == 4)
+        static_cast<float*>(p.Y)[n * p.ldy + r] = v;
+      else
+        static_cast<__nv_bfloat16*>(p.Y)[n * p.ldy + r] = __float2bfloat16_rn(v);
+    }
+  }
+}
+
+template <typename T, int FMT>
+kq_status launch_quantize(const QuantParams& p, cudaStream_t st) {
+  constexpr int R = 4;
+  QuantParams q = p;
+  q.units = kq::cdiv(p.rows, 128) * (128 / R) * p.chunks;
+  const int64_t grid = std::min<int64_t>(kq::cdiv(q.units, 8), 148 * 8);
+  quantize_kernel<T, FMT, R><<<(unsigned)grid, 256, 0, st>>>(q);
+  return kq::launch_check("kq_fp4_quantize");
+}
+
+template <typename T, int FMT>
+kq_status launch_matvec(const MatvecParams& p, cudaStream_t st) {
+  matvec_kernel<T, FMT><<<(unsigned)kq::cdiv(p.d_out, 16), kWarps * 32, 0, st>>>(p);
+  return kq::launch_check("kq_fp4_matvec");
+}
+
+}  // namespace
+
+extern "C" size_t kq_fp4_scale_bytes(int64_t rows, int64_t cols, int format) {
+  if (rows < 0 || cols < 1 || (format != KQ_FP4_MX && format != KQ_FP4_NV)) return 0;
+  return (size_t)kq::cdiv(rows, 128) * (size_t)kq::fp4::scale_tiles(cols, format) * 512;
+}
+
+extern "C" kq_status kq_fp4_quantize(const void* M, int dtype, int64_t ldm, const kq_fp4* Q, float* M_hat, int64_t ldh,
+                                     int32_t* info, kq_stream_t stream) {
+  KQ_TRY(kq::fp4::check(Q, "kq_fp4_quantize", "Q"));
+  if (dtype != KQ_F32 && dtype != KQ_BF16) return kq::fail(KQ_ERR_INVALID_ARG, "kq_fp4_quantize: dtype must be KQ_F32 or KQ_BF16");
+  if (!info) return kq::fail(KQ_ERR_INVALID_ARG, "kq_fp4_quantize: NULL pointer");
+  if (Q->rows == 0) {
+    kq::clear_error();
+    return KQ_OK;
+  }
+  if (!M) return kq::fail(KQ_ERR_INVALID_ARG, "kq_fp4_quantize: NULL pointer");
+  if (Q->format == KQ_FP4_NV && !Q->gscale) return kq::fail(KQ_ERR_INVALID_ARG, "kq_fp4_quantize: KQ_FP4_NV needs gscale");
+  const size_t esize = dtype == KQ_F32 ? 4 : 2;
+  if (ldm < Q->cols || (M_hat && ldh < Q->cols)) return kq::fail(KQ_ERR_INVALID_ARG, "kq_fp4_quantize: leading dimension too small");
+  if (!kq::aligned(M, esize) || (M_hat && !kq::aligned(M_hat, 4)))
+    return kq::fail(KQ_ERR_ALIGNMENT, "kq_fp4_quantize: M and M_hat aligned to their elements");
+  QuantParams p = {};
+  p.rows = Q->rows;
+  p.cols = Q->cols;
+  p.ldm = ldm;
+  p.ldc = Q->ld;
+  p.ldh = ldh;
+  p.kat = kq::fp4::scale_tiles(Q->cols, Q->format);
+  p.chunks = kq::cdiv(p.kat * 4 * block_of(Q->format), 256);
+  p.M = M;
+  p.g = Q->gscale;
+  p.codes = Q->codes;
+  p.scales = Q->scales;
+  p.M_hat = M_hat;
+  p.m_vec = kq::aligned(M, 16) && (ldm * (int64_t)esize) % 16 == 0;
+  p.h_vec = kq::aligned(M_hat, 16) && ldh % 4 == 0;
+  p.info = info;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == KQ_F32)
+    KQ_TRY(Q->format == KQ_FP4_MX ? (launch_quantize<float, KQ_FP4_MX>(p, st)) : (launch_quantize<float, KQ_FP4_NV>(p, st)));
+  else
+    KQ_TRY(Q->format == KQ_FP4_MX ? (launch_quantize<__nv_bfloat16, KQ_FP4_MX>(p, st))
+                                  : (launch_quantize<__nv_bfloat16, KQ_FP4_NV>(p, st)));
+  kq::clear_error();
+  return KQ_OK;
+}
+
+extern "C" kq_status kq_fp4_matvec(const kq_fp4* W, const void* X, int dtype, int64_t ldx, int batch, void* Y, int64_t ldy,
+                                   kq_stream_t stream) {
+  KQ_TRY(kq::fp4::check(W, "kq_fp4_matvec", "W"));
+  if (dtype != KQ_F32 && dtype != KQ_BF16) return kq::fail(KQ_ERR_INVALID_ARG, "kq_fp4_matvec: dtype must be KQ_F32 or KQ_BF16");
+  if (batch < 1 || batch > 8) return kq::fail(KQ_ERR_UNSUPPORTED_SHAPE, "kq_fp4_matvec: batch outside 1..8");
+  if (W->rows == 0) {
+    kq::clear_error();
+    return KQ_OK;
+  }
+  if (!X || !Y) return kq::fail(KQ_ERR_INVALID_ARG, "kq_fp4_matvec: NULL pointer");
+  if (ldx < W->cols || ldy < W->rows) return kq::fail(KQ_ERR_INVALID_ARG, "kq_fp4_matvec: leading dimension too small");
+  const size_t esize = dtype == KQ_F32 ? 4 : 2;
+  if (!kq::aligned(X, esize) || !kq::aligned(Y, esize))
+    return kq::fail(KQ_ERR_ALIGNMENT, "kq_fp4_matvec: X and Y aligned to their elements");
+  MatvecParams p = {};
+  p.codes = W->codes;
+  p.scales = W->scales;
+  p.g = W->gscale;
+  p.d_out = W->rows;
+  p.d_in = W->cols;
+  p.ldc = W->ld;
+  p.kat = kq::fp4::scale_tiles(W->cols, W->format);
+  p.X = X;
+  p.ldx = ldx;
+  p.x_vec = kq::aligned(X, 16) && (batch == 1 || (ldx * (int64_t)esize) % 16 == 0);
+  p.batch = batch;
+  p.Y = Y;
+  p.ldy = ldy;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == KQ_F32)
+    KQ_TRY(W->format == KQ_FP4_MX ? (launch_matvec<float, KQ_FP4_MX>(p, st)) : (launch_matvec<float, KQ_FP4_NV>(p, st)));
+  else
+    KQ_TRY(W->format == KQ_FP4_MX ? (launch_matvec<__nv_bfloat16, KQ_FP4_MX>(p, st))
+                                  : (launch_matvec<__nv_bfloat16, KQ_FP4_NV>(p, st)));
+  kq::clear_error();
+  return KQ_OK;
+}

@@ -35,6 +35,13 @@ class BitResult:
     perm: torch.Tensor = None
 
 
+@dataclasses.dataclass
+class Fp4Result:
+    matrix: K.Fp4Matrix     # codes and block scales of the rotated weights
+    W_hat: torch.Tensor     # the fp32 values they stand for
+    loss: torch.Tensor      # fp64[1] device
+
+
 class LayerQuantizer:
     """Device buffers for one (d_out, d_in) layer and the calls that fill them."""
 
@@ -209,7 +216,103 @@ class LayerQuantizer:
         self.loss_all(results, stream)
         return results
 
+    def quantize_fp4(self, format, stream=None):
+        """W' (after rotate()) on a microscaled 4-bit floating-point grid,
+        rounded to nearest, and the Kronecker loss of that: the format of the
+        tensor cores beside the integer settings of quantize_all()."""
+        g = global_scale(self.Wp) if format == K.KQ_FP4_NV else None
+        res = Fp4Result(None, torch.empty_like(self.Wp), torch.zeros(1, dtype=torch.float64, device=self.device))
+        res.matrix = K.kq_fp4_quantize(self.Wp, format, g, M_hat=res.W_hat, info=self.info, stream=stream)
+        self.loss(res, stream)
+        return res
+
     def check(self, where="kronq"):
+        K.check_info(self.info, where)
+
+
+def global_scale(M):
+    """The KQ_FP4_NV global scale of a matrix (or of activations like it): its
+    largest element at code 6 under the largest block scale, 448.  Stays on
+    the device; runs on the current stream."""
+    return (M.abs().amax().float() / (6.0 * 448.0)).clamp_min(torch.finfo(torch.float32).tiny).reshape(1)
+
+
+class GatedCalibration:
+    """Covariances of a gated MLP's linears, H = act(X Wg^T) * (X Wu^T) and the
+    down projection Y = H Wd^T, from token batches.
+
+    kq_gated_ffn_backward turns X and dH (the gradient at the down
+    projection's input) into the tensors the covariances are taken of: H (input
+    of down), dG and dU (output gradients of gate and up), and dX for the
+    layers before.  H_X is shared by gate and up (KronQ review, Background:
+    H ~ H_X kron H_G; KronQ paper page, authors' reply: H_G from one backward
+    pass)."""
+
+    def __init__(self, d_model, d_ff, device="cuda"):
+        dev = torch.device(device)
+        f32 = dict(dtype=torch.float32, device=dev)
+        self.H_X = torch.zeros((d_model, d_model), **f32)
+        self.H_X_down = torch.zeros((d_ff, d_ff), **f32)
+        self.H_G_gate = torch.zeros((d_ff, d_ff), **f32)
+        self.H_G_up = torch.zeros((d_ff, d_ff), **f32)
+        self.d_model, self.d_ff, self.device = d_model, d_ff, dev
+        self.info = K.new_info(dev)
+        self._ws = K.workspace(256, dev)
+
+    def add(self, X, W_gate, W_up, dH, n_total, act=K.KQ_ACT_SILU, need_dX=True, stream=None):
+        """One batch of tokens; n_total: the tokens of all batches.  Returns dX (or None)."""
+        ld = -(-self.d_ff // 8) * 8
+        H = torch.empty((X.shape[0], ld), dtype=torch.bfloat16, device=self.device)[:, :self.d_ff]
+        dG, dU, dX, _, _ = K.kq_gated_ffn_backward(X, W_gate, W_up, dH, act, H=H, need_dX=need_dX, need_dW=False,
+                                                   info=self.info, stream=stream)
+        need = max(K.kq_accum_cov_workspace_size(X.shape[0], d) for d in (self.d_model, self.d_ff))
+        if need > self._ws.numel():
+            self._ws = K.workspace(need, self.device)
+        for A, C in ((X, self.H_X), (H, self.H_X_down), (dG, self.H_G_gate), (dU, self.H_G_up)):
+            K.kq_accum_cov(A, C, 1.0 / n_total, True, self._ws, self.info, stream)
+        return dX
+
+    def check(self, where="gated calibration"):
+        K.check_info(self.info, where)
+
+
+class Fp4MLP:
+    """A gated MLP served in microscaled 4-bit: Y = (act(X Wg^T) * (X Wu^T)) Wd^T
+    with weights and activations quantized (kq_fp4_quantize, kq_fp4_gated_ffn,
+    kq_fp4_quantize, kq_fp4_gemm), or up to 8 tokens through one linear
+    with its activations left as they are (decode())."""
+
+    def __init__(self, W_gate, W_up, W_down, format=K.KQ_FP4_MX, act=K.KQ_ACT_SILU):
+        self.format, self.act = format, act
+        self.device = W_gate.device
+        self.info = K.new_info(self.device)
+        nv = format == K.KQ_FP4_NV
+        self.gate, self.up, self.down = (K.kq_fp4_quantize(W, format, global_scale(W) if nv else None, info=self.info)
+                                         for W in (W_gate, W_up, W_down))
+        self.g_x = self.g_h = None
+
+    def calibrate(self, X):
+        """The activations' global scales (KQ_FP4_NV) from calibration tokens X."""
+        if self.format == K.KQ_FP4_NV:
+            self.g_x = global_scale(X)
+            self.g_h = global_scale(self._hidden(X, None))
+
+    def _hidden(self, X, stream):
+        Xq = K.kq_fp4_quantize(X, self.format, self.g_x, info=self.info, stream=stream)
+        return K.kq_fp4_gated_ffn(Xq, self.gate, self.up, self.act, info=self.info, stream=stream)
+
+    def __call__(self, X, stream=None):
+        """X bf16 or float32 [tokens, d] -> Y bf16 [tokens, d]."""
+        if self.format == K.KQ_FP4_NV and self.g_x is None:
+            raise RuntimeError("KQ_FP4_NV needs calibrate() first")
+        Hq = K.kq_fp4_quantize(self._hidden(X, stream), self.format, self.g_h, info=self.info, stream=stream)
+        return K.kq_fp4_gemm(Hq, self.down, info=self.info, stream=stream)
+
+    def decode(self, linear, X, stream=None):
+        """X W^T of linear "gate", "up" or "down" for 1..8 unquantized vectors."""
+        return K.kq_fp4_matvec(getattr(self, linear), X, stream=stream)
+
+    def check(self, where="fp4 mlp"):
         K.check_info(self.info, where)
 
 
