@@ -6,9 +6,16 @@
 // e2m1 codes: kind::mxf4 (one E8M0 scale per 32 codes) and kind::mxf4nvf4 (one
 // E4M3 scale per 16).  In all of them a pipeline stage holds 128 bytes of K
 // per row (64 bf16 or 256 codes, four MMA steps of 32 bytes) in the 128-byte
-// swizzle.  Scale bytes travel as whole 512-byte tiles (128 rows x 4 blocks,
-// the layout that tcgen05.cp 32x128b.warpx4 takes), shared memory -> TMEM
-// beside the MMAs that use them.
+// swizzle.  Scale bytes travel as whole 512-byte tiles (128 rows x 4 blocks) by
+// TMA to shared memory and from there to TMEM in one of two ways.  CG = 2: the
+// issuing thread's tcgen05.cp, which runs in turn with the MMAs at about 53
+// cycles a tile (6 tiles, KQ_FP4_MX, or 12, KQ_FP4_NV, beside the 512 MMA cycles
+// of a stage: 0.61 and 0.82 us a stage against 0.43 without them, at 8192 x
+// 11008 x 16384).  CG = 1: the epilogue's four warps, one per lane quarter, with
+// tcgen05.st (the 16 bytes of a tile row are a lane's four columns): it leaves
+// the issue order alone and takes half the columns where an MMA needs half a
+// tile.  Under a dense stream of MMAs these stores wait for TMEM (0.87 us a
+// stage at the size above), so the pair does not use them.
 //
 // Shapes.  CG = 2: a CTA pair per 256 x 256 tile (cta_group::2), each CTA
 // holding 128 rows of A and of B, so an SM fetches 64 bytes per MMA cycle
@@ -22,7 +29,11 @@
 // second the up rows; with CG = 1 two MMAs per step.  The epilogue then has
 // both projections of a feature in one thread.
 //
-// Warp roles: 0 TMA, 1 TMEM and MMA issue, 2.. epilogue (one lane per row).
+// Warp roles: 0 TMA, 1 TMEM and MMA issue, the others the epilogue (one lane per
+// row, output through a swizzled staging buffer so that rows leave in full
+// 128-byte lines).  With CG = 2 bf16 has two accumulators used in turn; beside
+// the scales only one fits, which the epilogue takes into registers whole, so
+// that the next tile's MMAs wait for that read only.
 // Every mbarrier wait is bounded by a time limit; on expiry the kernel
 // records KQ_ERR_TIMEOUT, drains its copies (bounded), frees TMEM and returns.
 #pragma once
@@ -39,32 +50,39 @@ using namespace kq::tc;
 enum { KIND_BF16 = 0, KIND_MX = 1, KIND_NV = 2 };
 enum { EPI_STORE = 0, EPI_GATED = 1, EPI_GATED_BWD = 2 };
 
-template <int KIND_, int CG_, int BN_, bool AMN_, bool BMN_, int EPI_, int STAGES_, int EW_>
+template <int KIND_, int CG_, int BN_, bool AMN_, bool BMN_, int EPI_, int STAGES_>
 struct Cfg {
-  static constexpr int KIND = KIND_, CG = CG_, BN = BN_, EPI = EPI_, STAGES = STAGES_, EW = EW_;
+  static constexpr int KIND = KIND_, CG = CG_, BN = BN_, EPI = EPI_, STAGES = STAGES_;
   static constexpr bool AMN = AMN_, BMN = BMN_, FP4 = KIND != KIND_BF16, DUAL = EPI != EPI_STORE;
   static constexpr int NSUB = (CG == 1 && DUAL) ? 2 : 1;     // MMAs per K step
   static constexpr int MMA_N = BN / NSUB;
   static constexpr int OUTC = DUAL ? BN / 2 : BN;            // output columns of a tile
-  static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / CG * 128;
+  static constexpr int B_BYTES = BN / CG * 128;
   static constexpr int ATOMS = KIND == KIND_MX ? 2 : (KIND == KIND_NV ? 4 : 0);   // scale tiles per stage and 128 rows
   static constexpr int SFB_TILES = DUAL ? 2 : (BN + 127) / 128;
   static constexpr int SFA_BYTES = ATOMS * 512, SFB_BYTES = SFB_TILES * ATOMS * 512;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
-  static constexpr int SF_COLS = ATOMS * 4 * (1 + SFB_TILES);
-  // scale buffers in TMEM: one per stage where they fit, else two (the MMA
-  // thread then waits for the stage before last)
-  static constexpr int NSF = !FP4 ? 0 : (CG == 2 ? STAGES : 2);
-  static constexpr int NBUF = (CG == 2 && 2 * BN + NSF * SF_COLS <= 512) ? 2 : 1;  // accumulators
-  static constexpr int COLS = NBUF * BN + NSF * SF_COLS;
+  // A comes last in a stage: with few rows its box, and the stage, are shorter
+  // (the MMA reads on into what follows: rows past M, whose results are not stored)
+  static constexpr int A_OFF = B_BYTES + SFA_BYTES + SFB_BYTES;
+  static constexpr int A_BYTES = 128 * 128;
+  // TMEM columns of a scale tile of B: a 64-column MMA takes half a tile's rows
+  static constexpr int SFB_W = MMA_N == 64 ? 2 : 4;
+  static constexpr int SF_COLS = ATOMS * (4 + SFB_W * SFB_TILES);
+  static constexpr int NBUF = (CG == 2 && !FP4) ? 2 : 1;     // accumulators
+  static constexpr int COLS = NBUF * BN + STAGES * SF_COLS;  // a scale buffer per stage
   static constexpr int TMEM_COLS = COLS <= 64 ? 64 : (COLS <= 128 ? 128 : (COLS <= 256 ? 256 : 512));
   static_assert(COLS <= 512, "TMEM");
-  static constexpr int THREADS = 64 + 32 * EW;
+  static constexpr int EW = CG == 2 ? 8 : 4;                 // epilogue warps
+  static constexpr int EW0 = 2;                              // the first of them
+  static constexpr int THREADS = 32 * (EW0 + EW);
   static constexpr int PART_LD = BN + 4;                     // row stride of the split-K partials
-  static constexpr int RING = STAGES * STAGE_BYTES;
-  static constexpr int SMEM = RING + 1024 + 256;
+  static constexpr int RING = STAGES * (A_OFF + A_BYTES);
+  static constexpr int STAGING = EW * 4096;                  // 32 rows x 128 bytes per epilogue warp
+  static constexpr int BARS = 1024;
+  // CG = 1 has one tile per CTA: staging and split-K partials reuse the ring
+  static constexpr int SMEM = 1024 + BARS + RING + (CG == 2 ? STAGING : 0);
   static_assert(SMEM <= 232448, "shared memory");
-  static_assert(CG == 2 || 128 * PART_LD * 4 <= RING, "split-K partials reuse the ring");
+  static_assert(CG == 2 || (128 * PART_LD * 4 <= RING && STAGING <= RING), "the ring holds what reuses it");
 };
 
 struct Maps {
@@ -116,24 +134,85 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
+// Arrivals come from both CTAs of a pair: acquire at cluster scope.
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// The same without the hardware's own short wait.
+__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Bounded wait of a whole warp with the contract of mbar_wait (limit 0: give up
+// at the first poll that finds the phase incomplete); every lane gets the same
+// answer, so the control flow around it stays uniform.  The clock is read only
+// after a run of plain polls: reading it costs more than a pipeline stage
+// takes, and a wait in a running pipeline ends within a few polls.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* info, int where,
+                                          unsigned long long limit_ns) {
+  if (limit_ns == 0) {
+    if (__all_sync(0xffffffffu, test_wait(bar, parity))) return true;
+    if (threadIdx.x % 32 == 0 && !*abort_flag) {
+      *abort_flag = 1;
+      report(info, KQ_ERR_TIMEOUT, where);
+    }
+    return false;
+  }
+  for (int i = 0; i < 65; ++i)
+    if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
+  bool ok = true;
+  if (threadIdx.x % 32 == 0) ok = mbar_wait(bar, parity, abort_flag, info, where, limit_ns);
+  ok = __all_sync(0xffffffffu, ok);
+  return ok && __all_sync(0xffffffffu, try_wait(bar, parity));   // every lane acquires
+}
+
+// The issuing warps run their loops as whole warps and predicate only the
+// tcgen05 and TMA instructions on one lane (`on`): their operands then stay in
+// uniform registers, as the instructions want them.
+
 // A TMA tile load; with CG = 2 the barrier may be the pair leader's.
 template <int CG>
-__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  if constexpr (CG == 2) {
+__device__ __forceinline__ void load_2d(uint32_t on, uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if constexpr (CG == 2)
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-        "[%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(on)
         : "memory");
-  } else {
-    tma_load_2d(dst, map, x, y, bar);
-  }
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(on)
+        : "memory");
 }
 
 template <int CG, int NCOLS>
@@ -155,61 +234,102 @@ __device__ __forceinline__ void free_tmem(uint32_t taddr) {
 
 // Arrive on `bar` (of both CTAs of a pair) once the MMAs and copies issued so far are done.
 template <int CG>
-__device__ __forceinline__ void commit(uint32_t bar) {
+__device__ __forceinline__ void commit(uint32_t on, uint32_t bar) {
   if constexpr (CG == 2)
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+        "h"((uint16_t)3), "r"(on)
         : "memory");
   else
-    mma_commit(bar);
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(on)
+        : "memory");
 }
 
 // The same on this CTA's barrier alone.
 template <int CG>
-__device__ __forceinline__ void commit_local(uint32_t bar) {
+__device__ __forceinline__ void commit_local(uint32_t on, uint32_t bar) {
   if constexpr (CG == 2)
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(on)
+        : "memory");
   else
-    mma_commit(bar);
+    commit<1>(on, bar);
 }
 
+#define KQ_MMA_BF16(CGN)                                                                                             \
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"                          \
+               "@q tcgen05.mma.cta_group::" CGN ".kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),                     \
+               "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on)                                                         \
+               : "memory")
+
 template <int CG>
-__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_bf16(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   if constexpr (CG == 2)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
+    KQ_MMA_BF16("2");
   else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
+    KQ_MMA_BF16("1");
 }
 
 #define KQ_MMA_FP4(CGN, KINDVEC)                                                                                     \
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                                      \
-               "tcgen05.mma.cta_group::" CGN "." KINDVEC " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),            \
-               "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)                                               \
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"                          \
+               "@q tcgen05.mma.cta_group::" CGN "." KINDVEC " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),         \
+               "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc), "r"(on)                                      \
                : "memory")
 
 template <int KIND, int CG>
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                        uint32_t acc) {
+__device__ __forceinline__ void mma_fp4(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, uint32_t acc) {
   if constexpr (KIND == KIND_MX && CG == 1) KQ_MMA_FP4("1", "kind::mxf4.block_scale.scale_vec::2X");
   if constexpr (KIND == KIND_MX && CG == 2) KQ_MMA_FP4("2", "kind::mxf4.block_scale.scale_vec::2X");
   if constexpr (KIND == KIND_NV && CG == 1) KQ_MMA_FP4("1", "kind::mxf4nvf4.block_scale.scale_vec::4X");
   if constexpr (KIND == KIND_NV && CG == 2) KQ_MMA_FP4("2", "kind::mxf4nvf4.block_scale.scale_vec::4X");
 }
 
-// One 512-byte scale tile to 4 TMEM columns, repeated in the four lane quarters.
-template <int CG>
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
-  if constexpr (CG == 2)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-  else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+// N words per lane to N TMEM columns of the warp's lane quarter.
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* v) {
+  if constexpr (N == 4)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3])
+                 : "memory");
+  else if constexpr (N == 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  else {
+    static_assert(N % 16 == 0, "4, 8 or a multiple of 16 columns");
+#pragma unroll
+    for (int i = 0; i < N; i += 16)
+      asm volatile(
+          "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+              taddr + i),
+          "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7]),
+          "r"(v[i + 8]), "r"(v[i + 9]), "r"(v[i + 10]), "r"(v[i + 11]), "r"(v[i + 12]), "r"(v[i + 13]), "r"(v[i + 14]),
+          "r"(v[i + 15])
+          : "memory");
+  }
+}
+
+// One 512-byte scale tile to 4 TMEM columns, repeated in the four lane quarters
+// of both CTAs of a pair.
+__device__ __forceinline__ void copy_scales_pair(uint32_t on, uint32_t taddr, uint64_t desc) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(desc), "r"(on)
+      : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // Instruction descriptor of the block-scaled kinds: scale ids (which half of
@@ -220,18 +340,19 @@ constexpr uint32_t idesc_fp4(bool e8m0, uint32_t M, uint32_t N, uint32_t sf_id) 
          (sf_id << 29);
 }
 
-// 32 lanes x 32 consecutive 32-bit columns.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+// 32 lanes x 32 consecutive 32-bit columns, waited for.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   uint32_t r[32];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+      : "r"(taddr)
+      : "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
@@ -257,97 +378,118 @@ __device__ __forceinline__ Gate gate_of(float g, int act) {
   return {__fdividef(1.f, 1.f + __expf(-z)), dz};
 }
 
-// ------------------------------------------------------------------ stores
+// ------------------------------------------------------------------ output
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-
-// v[0..n) to bf16 columns c0.. of a row (n a multiple of 8), columns below N only.
-template <int n>
-__device__ __forceinline__ void store_bf16(__nv_bfloat16* row, int64_t c0, int64_t N, int vec, const float* v) {
-  if (vec && c0 + n <= N) {
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+__device__ __forceinline__ void unpack8(uint4 q, float* v) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int i = 0; i < n; i += 8)
-      *reinterpret_cast<uint4*>(row + c0 + i) = make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]),
-                                                           pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < n; ++i)
-      if (c0 + i < N) row[c0 + i] = __float2bfloat16_rn(v[i]);
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
   }
 }
 
-template <int n>
-__device__ __forceinline__ void store_f32(float* row, int64_t c0, int64_t N, int vec, const float* v) {
-  if (vec && c0 + n <= N) {
-#pragma unroll
-    for (int i = 0; i < n; i += 4) *reinterpret_cast<float4*>(row + c0 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+// 16 bytes of a row from column c, only the elements below N.
+template <typename T>
+__device__ __forceinline__ void store16(T* row, int64_t c, int64_t N, int vec, uint4 q) {
+  constexpr int E = 16 / sizeof(T);
+  if (vec && c + E <= N) {
+    *reinterpret_cast<uint4*>(row + c) = q;
   } else {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int i = 0; i < n; ++i)
-      if (c0 + i < N) row[c0 + i] = v[i];
-  }
-}
-
-template <int n>
-__device__ __forceinline__ void load_bf16(const __nv_bfloat16* row, int64_t c0, int64_t N, int vec, float* v) {
-  if (vec && c0 + n <= N) {
-#pragma unroll
-    for (int i = 0; i < n; i += 8) {
-      const uint4 q = *reinterpret_cast<const uint4*>(row + c0 + i);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[i + 2 * j] = __uint_as_float(w[j] << 16);
-        v[i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-      }
+    for (int e = 0; e < E; ++e) {
+      if (c + e >= N) break;
+      if constexpr (sizeof(T) == 4)
+        row[c + e] = __uint_as_float(w[e]);
+      else
+        row[c + e] = __ushort_as_bfloat16((unsigned short)(w[e / 2] >> (16 * (e & 1))));
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < n; ++i) v[i] = c0 + i < N ? __bfloat162float(row[c0 + i]) : 0.f;
   }
 }
+__device__ __forceinline__ uint4 load16(const __nv_bfloat16* row, int64_t c, int64_t N, int vec) {
+  if (vec && c + 8 <= N) return *reinterpret_cast<const uint4*>(row + c);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (c + e < N) w[e / 2] |= (uint32_t)__bfloat16_as_ushort(row[c + e]) << (16 * (e & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
-// n output columns c0.. of row r from the accumulators (a: the product, or the
-// gate projection; u: the up projection), scaled by sa and su.
-template <int EPI, int n>
-__device__ __forceinline__ void finish(const Params& p, int problem, int64_t r, int64_t c0, float sa, float su, float* a,
-                                       float* u) {
+// A warp's staging: 32 rows of 128 bytes; 16-byte piece k of row i lies at
+// piece k ^ (i % 8), so that rows and lines are both free of bank conflicts.
+__device__ __forceinline__ uint32_t piece(uint32_t stg, int i, int k) { return stg + 128 * i + 16 * (k ^ (i & 7)); }
+
+// The staged rows (row 0 = row r0 of the matrix, columns c0..) to global memory,
+// 4 rows of 128 bytes per step; or from it.
+template <typename T>
+__device__ __forceinline__ void rows_out(uint32_t stg, T* base, int64_t ld, int64_t r0, int64_t M, int64_t c0, int64_t N, int vec) {
+  const int lane = threadIdx.x % 32, k = lane % 8;
+  __syncwarp();
+#pragma unroll 2
+  for (int i = lane / 8; i < 32; i += 4)
+    if (r0 + i < M) store16(base + (r0 + i) * ld, c0 + k * (16 / (int)sizeof(T)), N, vec, lds128(piece(stg, i, k)));
+  __syncwarp();
+}
+__device__ __forceinline__ void rows_in(uint32_t stg, const __nv_bfloat16* base, int64_t ld, int64_t r0, int64_t M, int64_t c0,
+                                        int64_t N, int vec) {
+  const int lane = threadIdx.x % 32, k = lane % 8;
+  __syncwarp();
+#pragma unroll 2
+  for (int i = lane / 8; i < 32; i += 4)
+    sts128(piece(stg, i, k), r0 + i < M ? load16(base + (r0 + i) * ld, c0 + 8 * k, N, vec) : make_uint4(0, 0, 0, 0));
+  __syncwarp();
+}
+
+struct Grads {
+  float g, u, h;
+};
+// dG = dH u act'(g), dU = dH act(g), and H.
+__device__ __forceinline__ Grads gate_backward(float g, float u, float dh, int act) {
+  const Gate q = gate_of(g, act);
+  const float a = g * q.p;
+  return {dh * u * fmaf(a * (1.f - q.p), q.dz, q.p), dh * a, a * u};
+}
+
+// Eight output columns c.. of row r (the split-K sums).
+template <int EPI>
+__device__ __forceinline__ void finish8(const Params& p, int problem, int64_t r, int64_t c, float sa, float su, float* a, float* u) {
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out[problem]) + r * p.ldo[problem];
   if constexpr (EPI == EPI_STORE) {
 #pragma unroll
-    for (int i = 0; i < n; ++i) a[i] *= sa;
-    if (p.out_f32)
-      store_f32<n>(static_cast<float*>(p.out[problem]) + r * p.ldo[problem], c0, p.N, p.out_vec[problem], a);
-    else
-      store_bf16<n>(static_cast<__nv_bfloat16*>(p.out[problem]) + r * p.ldo[problem], c0, p.N, p.out_vec[problem], a);
+    for (int i = 0; i < 8; ++i) a[i] *= sa;
+    if (p.out_f32) {
+      float* f = static_cast<float*>(p.out[problem]) + r * p.ldo[problem];
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(a);
+      store16(f, c, p.N, p.out_vec[problem], make_uint4(w[0], w[1], w[2], w[3]));
+      store16(f, c + 4, p.N, p.out_vec[problem], make_uint4(w[4], w[5], w[6], w[7]));
+    } else {
+      store16(out, c, p.N, p.out_vec[problem], pack8(a));
+    }
   } else if constexpr (EPI == EPI_GATED) {
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float g = sa * a[i];
-      a[i] = g * gate_of(g, p.act).p * (su * u[i]);
-    }
-    store_bf16<n>(static_cast<__nv_bfloat16*>(p.out[0]) + r * p.ldo[0], c0, p.N, p.out_vec[0], a);
+    for (int i = 0; i < 8; ++i) a[i] = (sa * a[i]) * gate_of(sa * a[i], p.act).p * (su * u[i]);
+    store16(out, c, p.N, p.out_vec[0], pack8(a));
   } else {
-    float dh[n];
-    load_bf16<n>(p.dh + r * p.lddh, c0, p.N, p.dh_vec, dh);
-    if (p.h) {
-      float h[n];
+    float dh[8], h[8];
+    unpack8(load16(p.dh + r * p.lddh, c, p.N, p.dh_vec), dh);
 #pragma unroll
-      for (int i = 0; i < n; ++i) h[i] = a[i] * gate_of(a[i], p.act).p * u[i];
-      store_bf16<n>(p.h + r * p.ldh, c0, p.N, p.h_vec, h);
+    for (int i = 0; i < 8; ++i) {
+      const Grads q = gate_backward(a[i], u[i], dh[i], p.act);
+      a[i] = q.g;
+      u[i] = q.u;
+      h[i] = q.h;
     }
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float g = a[i];
-      const Gate q = gate_of(g, p.act);
-      // dG = dH u act'(g), dU = dH act(g)
-      a[i] = dh[i] * u[i] * fmaf(g * q.p * (1.f - q.p), q.dz, q.p);
-      u[i] = dh[i] * (g * q.p);
-    }
-    store_bf16<n>(static_cast<__nv_bfloat16*>(p.out[0]) + r * p.ldo[0], c0, p.N, p.out_vec[0], a);
-    store_bf16<n>(static_cast<__nv_bfloat16*>(p.out[1]) + r * p.ldo[1], c0, p.N, p.out_vec[1], u);
+    store16(out, c, p.N, p.out_vec[0], pack8(a));
+    store16(static_cast<__nv_bfloat16*>(p.out[1]) + r * p.ldo[1], c, p.N, p.out_vec[1], pack8(u));
+    if (p.h) store16(p.h + r * p.ldh, c, p.N, p.h_vec, pack8(h));
   }
 }
 
@@ -363,19 +505,54 @@ __device__ __forceinline__ void tile_coords(const Params& p, int t, int* tm, int
   *tn = r / w;
 }
 
+// The scale tiles of a stage from shared memory to this warp's lane quarter of TMEM.
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 1) tile_kernel(const __grid_constant__ Maps maps, const Params p) {
+__device__ __forceinline__ void scales_to_tmem(uint32_t sf, uint32_t taddr, int upper_half) {
+  const int lane = threadIdx.x % 32;
+  uint32_t v[4 * C::ATOMS], w[C::SFB_W * C::SFB_TILES * C::ATOMS];
+#pragma unroll
+  for (int q = 0; q < C::ATOMS; ++q) {
+    const uint4 x = lds128(sf + 512 * q + 16 * lane);
+    v[4 * q] = x.x;
+    v[4 * q + 1] = x.y;
+    v[4 * q + 2] = x.z;
+    v[4 * q + 3] = x.w;
+#pragma unroll
+    for (int b = 0; b < C::SFB_TILES; ++b) {   // one K tile's columns side by side
+      const uint4 y = lds128(sf + C::SFA_BYTES + 512 * (C::ATOMS * b + q) + 16 * lane);
+      uint32_t* d = w + C::SFB_W * (C::SFB_TILES * q + b);
+      if constexpr (C::SFB_W == 4) {
+        d[0] = y.x;
+        d[1] = y.y;
+        d[2] = y.z;
+        d[3] = y.w;
+      } else {
+        d[0] = upper_half ? y.z : y.x;
+        d[1] = upper_half ? y.w : y.y;
+      }
+    }
+  }
+  tmem_st<4 * C::ATOMS>(taddr, v);
+  tmem_st<C::SFB_W * C::SFB_TILES * C::ATOMS>(taddr + 4 * C::ATOMS, w);
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(const __grid_constant__ Maps maps, const Params p) {
   constexpr int S = C::STAGES, CG = C::CG;
+  constexpr bool DRAIN = C::FP4 && CG == 2;   // one accumulator: read out whole before the stores
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RING);
-  // bars: full [0, S), empty [S, 2S), acc full [2S, 2S + 2), acc empty [2S + 2, 2S + 4), drained [2S + 4]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
+  // bars: full [0, S), empty [S, 2S), scales landed [2S, 3S), scales in TMEM
+  // [3S, 4S), acc full [4S, 4S + 2), acc empty [4S + 2, 4S + 4), drained [4S + 4]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * S + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + S);
-  const uint32_t accfull0 = smem_u32(bars + 2 * S), accempty0 = smem_u32(bars + 2 * S + 2);
-  const uint32_t drained = smem_u32(bars + 2 * S + 4);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S, landed0 = full0 + 16 * S, ready0 = full0 + 24 * S;
+  const uint32_t accfull0 = full0 + 32 * S, accempty0 = accfull0 + 16, drained = accfull0 + 32;
+  const uint32_t ring = full0 + C::BARS;
+  const uint32_t stage_bytes = (uint32_t)(C::A_OFF + 128 * p.a_rows);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int ks = CG == 1 ? p.ks : 1;
   const uint32_t crank = (CG == 2 || ks > 1) ? cluster_rank() : 0;
   const uint32_t rank = CG == 2 ? crank : 0;                  // CTA of the pair
@@ -388,10 +565,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) tile_kernel(const __grid_consta
     for (int s = 0; s < S; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
+      mbar_init(landed0 + 8 * s, 1);
+      mbar_init(ready0 + 8 * s, 4);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accfull0 + 8 * b, 1);
-      mbar_init(accempty0 + 8 * b, CG * C::EW * 32);
+      mbar_init(accempty0 + 8 * b, CG * C::EW);
     }
     mbar_init(drained, 1);
     *abort_flag = 0;
@@ -403,122 +582,130 @@ __global__ void __launch_bounds__(C::THREADS, 1) tile_kernel(const __grid_consta
   if (CG == 2 || ks > 1) cluster_sync();   // the other CTAs' barriers are ready too
   fence_after();
   const uint32_t tmem = *tmem_slot;
+  const uint32_t sf0 = tmem + C::NBUF * C::BN;
+
+  // The scales of stages kb0 .. kb1 of a tile, by one of the four warps that write them.
+  int sc_stage = 0;
+  uint32_t sc_phase = 0;
+  auto write_scales = [&](int tn) {
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!warp_wait(landed0 + 8 * sc_stage, sc_phase, abort_flag, p.info, 14, p.wait_ns)) return false;
+      // the slot's last MMAs are done: the producer waited for them before this stage's copies
+      fence_after();
+      if constexpr (C::FP4)
+        scales_to_tmem<C>(ring + sc_stage * stage_bytes + C::B_BYTES,
+                          sf0 + sc_stage * C::SF_COLS + ((uint32_t)(32 * (warp & 3)) << 16), tn & 1);
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ready0 + 8 * sc_stage);
+      if (++sc_stage == S) {
+        sc_stage = 0;
+        sc_phase ^= 1u;
+      }
+    }
+    return true;
+  };
 
   if (warp == 0) {
     // ---------------- TMA producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, issued_phase[S];
-      bool issued[S], ok = true;
-      for (int s = 0; s < S; ++s) issued[s] = false;
-      const uint32_t stage_tx = (uint32_t)(p.a_rows * 128 + C::B_BYTES + C::SFA_BYTES + C::SFB_BYTES) * CG;
-      for (int t = unit0; t < p.num_tiles && ok; t += units) {
-        const int problem = t / p.problem_tiles;
-        int tm, tn;
-        tile_coords(p, t - problem * p.problem_tiles, &tm, &tn);
-        const int m0 = tm * 128 * CG + (int)rank * 128, n0 = tn * C::OUTC;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.info, 11, p.wait_ns)) {
-            ok = false;
-            break;
-          }
-          uint32_t fb = full0 + 8 * stage;
-          if (CG == 1 || rank == 0) mbar_arrive_expect_tx(fb, stage_tx);
-          if (CG == 2) fb = mapa(fb, 0);
-          const uint32_t sa = smem_u32(smem + stage * C::STAGE_BYTES), sb = sa + C::A_BYTES;
-          const int seg = kb >= p.seg_blocks, k = kb - (seg ? p.seg_blocks : 0);
-          const CUtensorMap* ma = &maps.a[problem ? 1 : seg];
-          const CUtensorMap* mb = &maps.b[seg];
-          constexpr int KE = C::FP4 ? 128 : 64;   // map elements per stage along K (bytes of codes, or bf16)
-          if constexpr (C::AMN) {
-            load_2d<CG>(sa, ma, m0, 64 * k, fb);
-            load_2d<CG>(sa + 8192, ma, m0 + 64, 64 * k, fb);
-          } else {
-            load_2d<CG>(sa, ma, KE * k, m0, fb);
-          }
-          if constexpr (C::BMN) {
+    const uint32_t on = lane == 0;
+    int stage = 0;
+    uint32_t phase = 0, issued_phase = 0, issued = 0;   // bit s: stage s
+    bool ok = true;
+    const uint32_t stage_tx = (uint32_t)(p.a_rows * 128 + C::B_BYTES + (CG == 2 ? C::SFA_BYTES + C::SFB_BYTES : 0)) * CG;
+    for (int t = unit0; t < p.num_tiles && ok; t += units) {
+      const int problem = t / p.problem_tiles;
+      int tm, tn;
+      tile_coords(p, t - problem * p.problem_tiles, &tm, &tn);
+      const int m0 = tm * 128 * CG + (int)rank * 128, n0 = tn * C::OUTC;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!warp_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.info, 11, p.wait_ns)) {
+          ok = false;
+          break;
+        }
+        uint32_t fb = full0 + 8 * stage;
+        if (on && rank == 0) mbar_arrive_expect_tx(fb, stage_tx);
+        if (CG == 2) fb = mapa(fb, 0);
+        const uint32_t sb = ring + stage * stage_bytes, sa = sb + C::A_OFF;
+        const int seg = kb >= p.seg_blocks, k = kb - (seg ? p.seg_blocks : 0);
+        const CUtensorMap* ma = &maps.a[problem ? 1 : seg];
+        const CUtensorMap* mb = &maps.b[seg];
+        constexpr int KE = C::FP4 ? 128 : 64;   // map elements per stage along K (bytes of codes, or bf16)
+        if constexpr (C::FP4) {
+          const uint32_t sf = sb + C::B_BYTES, lb = CG == 2 ? fb : landed0 + 8 * stage;
+          if (CG == 1 && on) mbar_arrive_expect_tx(lb, C::SFA_BYTES + C::SFB_BYTES);
+          load_2d<CG>(on, sf, &maps.sfa, 0, (m0 / 128) * p.kat + kb * C::ATOMS, lb);
 #pragma unroll
-            for (int q = 0; q < C::BN / CG / 64; ++q)
-              load_2d<CG>(sb + 8192 * q, mb, n0 + (int)rank * (C::BN / CG) + 64 * q, 64 * k, fb);
-          } else if constexpr (C::DUAL && CG == 2) {
-            load_2d<CG>(sb, &maps.b[rank], KE * k, n0, fb);
-          } else if constexpr (C::DUAL) {
-            load_2d<CG>(sb, &maps.b[0], KE * k, n0, fb);
-            load_2d<CG>(sb + C::MMA_N * 128, &maps.b[1], KE * k, n0, fb);
-          } else {
-            load_2d<CG>(sb, mb, KE * k, n0 + (int)rank * (C::BN / CG), fb);
-          }
-          if constexpr (C::FP4) {
-            const uint32_t sf = sb + C::B_BYTES;
-            load_2d<CG>(sf, &maps.sfa, 0, (m0 / 128) * p.kat + kb * C::ATOMS, fb);
+          for (int q = 0; q < C::SFB_TILES; ++q)
+            load_2d<CG>(on, sf + C::SFA_BYTES * (1 + q), C::DUAL ? &maps.sfb[q] : &maps.sfb[0], 0,
+                       (n0 / 128 + (C::DUAL ? 0 : q)) * p.kat + kb * C::ATOMS, lb);
+        }
+        if constexpr (C::AMN) {
+          load_2d<CG>(on, sa, ma, m0, 64 * k, fb);
+          load_2d<CG>(on, sa + 8192, ma, m0 + 64, 64 * k, fb);
+        } else {
+          load_2d<CG>(on, sa, ma, KE * k, m0, fb);
+        }
+        if constexpr (C::BMN) {
 #pragma unroll
-            for (int q = 0; q < C::SFB_TILES; ++q)
-              load_2d<CG>(sf + C::SFA_BYTES * (1 + q), C::DUAL ? &maps.sfb[q] : &maps.sfb[0], 0,
-                          (n0 / 128 + (C::DUAL ? 0 : q)) * p.kat + kb * C::ATOMS, fb);
-          }
-          issued[stage] = true;
-          issued_phase[stage] = phase;
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          for (int q = 0; q < C::BN / CG / 64; ++q)
+            load_2d<CG>(on, sb + 8192 * q, mb, n0 + (int)rank * (C::BN / CG) + 64 * q, 64 * k, fb);
+        } else if constexpr (C::DUAL && CG == 2) {
+          load_2d<CG>(on, sb, &maps.b[rank], KE * k, n0, fb);
+        } else if constexpr (C::DUAL) {
+          load_2d<CG>(on, sb, &maps.b[0], KE * k, n0, fb);
+          load_2d<CG>(on, sb + C::MMA_N * 128, &maps.b[1], KE * k, n0, fb);
+        } else {
+          load_2d<CG>(on, sb, mb, KE * k, n0 + (int)rank * (C::BN / CG), fb);
+        }
+        issued |= 1u << stage;
+        issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok && rank == 0) {
-        // the copies in flight land before the CTA (or pair) can exit
-        const unsigned long long t0 = globaltimer();
-        for (int s = 0; s < S; ++s)
-          while (issued[s] && !mbar_try_wait(full0 + 8 * s, issued_phase[s]) && globaltimer() - t0 < kTimeoutNs) {
-          }
+    }
+    if (!ok) {
+      // the copies in flight land before the CTA (or pair) can exit
+      const unsigned long long t0 = globaltimer();
+      for (int s = 0; s < S; ++s) {
+        if (!(issued >> s & 1u)) continue;
+        const uint32_t ph = issued_phase >> s & 1u;
+        while (rank == 0 && !try_wait(full0 + 8 * s, ph) && globaltimer() - t0 < kTimeoutNs) {
+        }
+        while (C::FP4 && CG == 1 && !try_wait(landed0 + 8 * s, ph) && globaltimer() - t0 < kTimeoutNs) {
+        }
       }
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer (the pair's first CTA)
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const uint32_t on = lane == 0;
       int stage = 0, buf = 0;
-      uint32_t phase = 0, acc_phase = 0, done = 0;   // done: stages issued so far
-      bool ok = true;
-      const uint32_t sf0 = tmem + C::NBUF * C::BN;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true, any = false;
       for (int t = unit0; t < p.num_tiles && ok; t += units) {
-        if (!mbar_wait(accempty0 + 8 * buf, acc_phase ^ 1u, abort_flag, p.info, 12, p.wait_ns)) {
-          ok = false;
-          break;
-        }
-        fence_after();
+        if (!warp_wait(accempty0 + 8 * buf, acc_phase ^ 1u, abort_flag, p.info, 12, p.wait_ns)) break;
         const uint32_t d = tmem + buf * C::BN;
-        // a 64-column MMA in the upper half of a 128-row scale tile takes its columns 2 and 3
-        int sfb_shift = 0;
-        if constexpr (C::FP4 && C::MMA_N == 64) {
-          int tm, tn;
-          tile_coords(p, t % p.problem_tiles, &tm, &tn);
-          sfb_shift = (tn & 1) ? 2 : 0;
-        }
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(full0 + 8 * stage, phase, abort_flag, p.info, 13, p.wait_ns)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sa = smem_u32(smem + stage * C::STAGE_BYTES), sb = sa + C::A_BYTES;
+          ok = warp_wait(full0 + 8 * stage, phase, abort_flag, p.info, 13, p.wait_ns);
+          if (C::FP4 && CG == 1 && ok) ok = warp_wait(ready0 + 8 * stage, phase, abort_flag, p.info, 16, p.wait_ns);
+          if (!ok) break;
+          fence_after();
+          const uint32_t sb = ring + stage * stage_bytes, sa = sb + C::A_OFF;
           if constexpr (C::FP4) {
-            const int slot = C::NSF == S ? stage : (int)(done % C::NSF);
-            if (C::NSF < S && done >= (uint32_t)C::NSF) {
-              // the MMAs that read this scale buffer last are done
-              const uint32_t j = done - C::NSF;
-              if (!mbar_wait(empty0 + 8 * (j % S), (j / S) & 1u, abort_flag, p.info, 14, p.wait_ns)) {
-                ok = false;
-                break;
+            const uint32_t ca = sf0 + stage * C::SF_COLS, cb = ca + 4 * C::ATOMS;
+            if constexpr (CG == 2) {
+              const uint32_t sf = sb + C::B_BYTES;
+#pragma unroll
+              for (int q = 0; q < C::ATOMS; ++q) {
+                copy_scales_pair(on, ca + 4 * q, smem_desc(sf + 512 * q, 128, 128, 0));
+#pragma unroll
+                for (int b = 0; b < C::SFB_TILES; ++b)   // one K tile's columns side by side
+                  copy_scales_pair(on, cb + 4 * (C::SFB_TILES * q + b),
+                                   smem_desc(sf + C::SFA_BYTES + 512 * (C::ATOMS * b + q), 128, 128, 0));
               }
-            }
-            fence_after();
-            const uint32_t sf = sb + C::B_BYTES;
-            const uint32_t ca = sf0 + slot * C::SF_COLS, cb = ca + 4 * C::ATOMS;
-#pragma unroll
-            for (int q = 0; q < C::ATOMS; ++q) {
-              copy_scales<CG>(ca + 4 * q, smem_desc(sf + 512 * q, 128, 128, 0));
-#pragma unroll
-              for (int b = 0; b < C::SFB_TILES; ++b)   // one K tile's columns side by side
-                copy_scales<CG>(cb + 4 * (C::SFB_TILES * q + b),
-                                smem_desc(sf + C::SFA_BYTES * (1 + b) + 512 * q, 128, 128, 0));
             }
             const int n = min(4, p.steps - 4 * kb);
 #pragma unroll
@@ -529,12 +716,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) tile_kernel(const __grid_consta
               const uint32_t acc = (kb > kb0 || j > 0) ? 1u : 0u;
 #pragma unroll
               for (int s = 0; s < C::NSUB; ++s)
-                mma_fp4<C::KIND, CG>(d + s * C::MMA_N, smem_desc(sa + 32 * j, 16, 1024, kSwizzle128),
+                mma_fp4<C::KIND, CG>(on, d + s * C::MMA_N, smem_desc(sa + 32 * j, 16, 1024, kSwizzle128),
                                      smem_desc(sb + s * C::MMA_N * 128 + 32 * j, 16, 1024, kSwizzle128), id,
-                                     ca + 4 * atom, cb + 4 * (C::SFB_TILES * atom + s) + sfb_shift, acc);
+                                     ca + 4 * atom, cb + C::SFB_W * (C::SFB_TILES * atom + s), acc);
             }
           } else {
-            fence_after();
             constexpr uint32_t id = idesc(kFmtBF16, C::AMN, C::BMN, 128 * CG, C::MMA_N);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -544,83 +730,186 @@ __global__ void __launch_bounds__(C::THREADS, 1) tile_kernel(const __grid_consta
 #pragma unroll
               for (int s = 0; s < C::NSUB; ++s) {
                 const uint32_t bs = sb + s * C::MMA_N * 128;
-                mma_bf16<CG>(d + s * C::MMA_N, da,
+                mma_bf16<CG>(on, d + s * C::MMA_N, da,
                              C::BMN ? smem_desc(bs + 2048 * j, 8192, 1024, kSwizzle128)
                                     : smem_desc(bs + 32 * j, 16, 1024, kSwizzle128),
                              id, acc);
               }
             }
           }
-          ++done;
-          commit<CG>(empty0 + 8 * stage);   // the stage is free once these MMAs have read it
+          any = true;
+          commit<CG>(on, empty0 + 8 * stage);   // the stage is free once these MMAs have read it
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        commit<CG>(accfull0 + 8 * buf);
+        commit<CG>(on, accfull0 + 8 * buf);
         if (++buf == C::NBUF) {
           buf = 0;
           acc_phase ^= 1u;
         }
       }
-      if (done) {
+      if (any) {
         // every MMA this thread issued has completed before TMEM is released
-        commit_local<CG>(drained);
-        mbar_drain(drained, 0);
+        commit_local<CG>(on, drained);
+        if (on) mbar_drain(drained, 0);
       }
     }
   } else {
     // ---------------- epilogue: lane quarter warp % 4, one row per lane
-    const int wq = warp & 3, half = (warp - 2) / 4;
-    const int row = 32 * wq + lane;
-    int buf = 0;
-    uint32_t acc_phase = 0;
+    const int wq = warp & 3, share = (warp - C::EW0) / 4;
+    constexpr int CW = C::OUTC / (C::EW / 4);   // output columns of this warp
+    constexpr int CH = CW < 64 ? CW : 64;       // taken 64 at a time
+    static_assert(CH == 64, "64 output columns at a time");
+    const uint32_t stg = (CG == 2 ? ring + C::RING : ring) + 4096 * (warp - C::EW0);
     const float sa = (p.ga ? *p.ga : 1.f) * (p.gb[0] ? *p.gb[0] : 1.f);
     const float su = (p.ga ? *p.ga : 1.f) * (p.gb[1] ? *p.gb[1] : 1.f);
+    int buf = 0;
+    uint32_t acc_phase = 0;
     for (int t = unit0; t < p.num_tiles; t += units) {
       const int problem = t / p.problem_tiles;
       int tm, tn;
       tile_coords(p, t - problem * p.problem_tiles, &tm, &tn);
-      const int64_t r = (int64_t)tm * 128 * CG + rank * 128 + row, c0 = (int64_t)tn * C::OUTC;
-      // one lane waits, the warp follows: every lane leaves together on abort
-      bool ready = true;
-      if (lane == 0) ready = mbar_wait(accfull0 + 8 * buf, acc_phase, abort_flag, p.info, 15, p.wait_ns);
-      if (!__shfl_sync(0xffffffffu, ready ? 1 : 0, 0)) break;
-      __syncwarp();
+      if constexpr (C::FP4 && CG == 1) {
+        if (!write_scales(tn)) break;
+      }
+      const int64_t r0 = (int64_t)tm * 128 * CG + rank * 128 + 32 * wq;   // lane 0's row
+      const int64_t c0 = (int64_t)tn * C::OUTC + share * CW;
+      if (!warp_wait(accfull0 + 8 * buf, acc_phase, abort_flag, p.info, 15, p.wait_ns)) break;
       fence_after();
-      const uint32_t d = tmem + ((uint32_t)(32 * wq) << 16) + buf * C::BN;
-      constexpr int CW = C::OUTC / (C::EW / 4);   // output columns of this warp
-      constexpr int CN = CW < 32 ? CW : 32;
+      const uint32_t d = tmem + ((uint32_t)(32 * wq) << 16) + buf * C::BN + share * CW;
+      auto release = [&] {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2)
+            mbar_arrive_cluster(mapa(accempty0 + 8 * buf, 0));
+          else
+            mbar_arrive(accempty0 + 8 * buf);
+        }
+      };
       if (ks > 1) {
         // fp32 partials to this CTA's shared memory, summed below
-        float* part = reinterpret_cast<float*>(smem);
+        float* part = reinterpret_cast<float*>(smem + C::BARS);
+        if (r0 < p.M) {
 #pragma unroll 1
-        for (int c = half * (C::BN / (C::EW / 4)); c < (half + 1) * (C::BN / (C::EW / 4)); c += 16) {
-          float v[16];
-          tmem_ld16(d + c, v);
-          if (r < p.M) {
+          for (int c = 0; c < C::BN; c += 16) {
+            float v[16];
+            tmem_ld16(d + c, v);
+            if (r0 + lane < p.M) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<float4*>(part + row * C::PART_LD + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+              for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4*>(part + (32 * wq + lane) * C::PART_LD + c + i) =
+                    make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
           }
         }
-      } else {
-        static_assert(CN == 32, "32 output columns at a time");
+        release();
+      } else if constexpr (C::EPI == EPI_STORE) {
+        auto put = [&](int c, float* v) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) v[i] *= sa;
+          if (p.out_f32) {
+#pragma unroll
+            for (int h = 0; h < 64; h += 32) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(v + h + 4 * k);
+                sts128(piece(stg, lane, k), make_uint4(w[0], w[1], w[2], w[3]));
+              }
+              rows_out(stg, static_cast<float*>(p.out[problem]), p.ldo[problem], r0, p.M, c0 + c + h, p.N, p.out_vec[problem]);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sts128(piece(stg, lane, k), pack8(v + 8 * k));
+            rows_out(stg, static_cast<__nv_bfloat16*>(p.out[problem]), p.ldo[problem], r0, p.M, c0 + c, p.N,
+                     p.out_vec[problem]);
+          }
+        };
+        if (DRAIN && !p.out_f32) {
+          uint4 q[CW / 8];
+#pragma unroll
+          for (int c = 0; c < CW; c += 64) {
+            float v[64];
+            tmem_ld32(d + c, v);
+            tmem_ld32(d + c + 32, v + 32);
+#pragma unroll
+            for (int i = 0; i < 64; ++i) v[i] *= sa;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) q[c / 8 + k] = pack8(v + 8 * k);
+          }
+          release();
+#pragma unroll
+          for (int c = 0; c < CW; c += 64) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sts128(piece(stg, lane, k), q[c / 8 + k]);
+            rows_out(stg, static_cast<__nv_bfloat16*>(p.out[problem]), p.ldo[problem], r0, p.M, c0 + c, p.N,
+                     p.out_vec[problem]);
+          }
+        } else {
 #pragma unroll 1
-        for (int c = half * CW; c < (half + 1) * CW; c += 32) {
-          float a[32], u[C::DUAL ? 32 : 1];
-          tmem_ld32(d + c, a);
-          if constexpr (C::DUAL) tmem_ld32(d + C::BN / 2 + c, u);
-          if (r < p.M) finish<C::EPI, 32>(p, problem, r, c0 + c, sa, su, a, u);
+          for (int c = 0; c < CW; c += 64) {
+            float v[64];
+            tmem_ld32(d + c, v);
+            tmem_ld32(d + c + 32, v + 32);
+            if (c + 64 == CW) release();
+            put(c, v);
+          }
+        }
+      } else if constexpr (C::EPI == EPI_GATED) {
+        float g[64], u[64];
+        tmem_ld32(d, g);
+        tmem_ld32(d + 32, g + 32);
+        tmem_ld32(d + C::BN / 2, u);
+        tmem_ld32(d + C::BN / 2 + 32, u + 32);
+        release();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+#pragma unroll
+          for (int i = 8 * k; i < 8 * k + 8; ++i) g[i] = (sa * g[i]) * gate_of(sa * g[i], p.act).p * (su * u[i]);
+          sts128(piece(stg, lane, k), pack8(g + 8 * k));
+        }
+        rows_out(stg, static_cast<__nv_bfloat16*>(p.out[0]), p.ldo[0], r0, p.M, c0, p.N, p.out_vec[0]);
+      } else {
+        rows_in(stg, p.dh, p.lddh, r0, p.M, c0, p.N, p.dh_vec);
+        uint4 og[8], ou[8], oh[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float g[32], u[32];
+          tmem_ld32(d + 32 * h, g);
+          tmem_ld32(d + C::BN / 2 + 32 * h, u);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float dh[8], vh[8];
+            unpack8(lds128(piece(stg, lane, 4 * h + k)), dh);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const Grads q = gate_backward(g[8 * k + i], u[8 * k + i], dh[i], p.act);
+              g[8 * k + i] = q.g;
+              u[8 * k + i] = q.u;
+              vh[i] = q.h;
+            }
+            og[4 * h + k] = pack8(g + 8 * k);
+            ou[4 * h + k] = pack8(u + 8 * k);
+            oh[4 * h + k] = pack8(vh);
+          }
+        }
+        release();
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sts128(piece(stg, lane, k), og[k]);
+        rows_out(stg, static_cast<__nv_bfloat16*>(p.out[0]), p.ldo[0], r0, p.M, c0, p.N, p.out_vec[0]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sts128(piece(stg, lane, k), ou[k]);
+        rows_out(stg, static_cast<__nv_bfloat16*>(p.out[1]), p.ldo[1], r0, p.M, c0, p.N, p.out_vec[1]);
+        if (p.h) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sts128(piece(stg, lane, k), oh[k]);
+          rows_out(stg, p.h, p.ldh, r0, p.M, c0, p.N, p.h_vec);
         }
       }
-      fence_before();
-      if (CG == 2)
-        mbar_arrive_cluster(mapa(accempty0 + 8 * buf, 0));
-      else
-        mbar_arrive(accempty0 + 8 * buf);
       if (++buf == C::NBUF) {
         buf = 0;
         acc_phase ^= 1u;
@@ -634,30 +923,45 @@ __global__ void __launch_bounds__(C::THREADS, 1) tile_kernel(const __grid_consta
     if (ks > 1) {
       // sum of the cluster's partials in rank order; each CTA takes a share of the tile's columns
       cluster_sync();
-      if (unit0 < p.num_tiles) {
-        const int problem = unit0 / p.problem_tiles;
-        int tm, tn;
-        tile_coords(p, unit0 - problem * p.problem_tiles, &tm, &tn);
-        const float sa = (p.ga ? *p.ga : 1.f) * (p.gb[0] ? *p.gb[0] : 1.f);
-        const float su = (p.ga ? *p.ga : 1.f) * (p.gb[1] ? *p.gb[1] : 1.f);
-        const int rows = (int)min((int64_t)128, p.M - (int64_t)tm * 128);
-        const int share = C::OUTC / ks;            // a multiple of 8
-        const uint32_t base = smem_u32(smem);
-        for (int i = threadIdx.x; i < rows * (share / 8); i += C::THREADS) {
-          const int rr = i / (share / 8), c = (int)crank * share + 8 * (i % (share / 8));
-          float a[8], u[8];
+      const int problem = unit0 / p.problem_tiles;
+      int tm, tn;
+      tile_coords(p, unit0 - problem * p.problem_tiles, &tm, &tn);
+      const float sa = (p.ga ? *p.ga : 1.f) * (p.gb[0] ? *p.gb[0] : 1.f);
+      const float su = (p.ga ? *p.ga : 1.f) * (p.gb[1] ? *p.gb[1] : 1.f);
+      const int rows = (int)min((int64_t)128, p.M - (int64_t)tm * 128);
+      const int cols = C::OUTC / ks;               // a multiple of 8
+      for (int i = threadIdx.x; i < rows * (cols / 8); i += C::THREADS) {
+        const int rr = i / (cols / 8), c = (int)crank * cols + 8 * (i % (cols / 8));
+        const uint32_t at = ring + 4u * (uint32_t)(rr * C::PART_LD + c);
+        float a[8], u[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) a[e] = u[e] = 0.f;
-          for (int q = 0; q < ks; ++q) {
-            const uint32_t src = mapa(base + 4u * (uint32_t)(rr * C::PART_LD + c), (uint32_t)q);
+        for (int e = 0; e < 8; ++e) a[e] = u[e] = 0.f;
+        // the loads of all CTAs' pieces are in flight together
+        float4 x[8][C::DUAL ? 4 : 2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              a[e] += ld_cluster(src + 4 * e);
-              if constexpr (C::DUAL) u[e] += ld_cluster(src + 2 * C::BN + 4 * e);
+        for (int q = 0; q < 8; ++q) {
+          if (q < ks) {
+            const uint32_t src = mapa(at, (uint32_t)q);
+            x[q][0] = ld_cluster(src);
+            x[q][1] = ld_cluster(src + 16);
+            if constexpr (C::DUAL) {
+              x[q][2] = ld_cluster(src + 2 * C::BN);
+              x[q][3] = ld_cluster(src + 2 * C::BN + 16);
             }
           }
-          finish<C::EPI, 8>(p, problem, (int64_t)tm * 128 + rr, (int64_t)tn * C::OUTC + c, sa, su, a, u);
         }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          if (q < ks) {
+            const float* f = reinterpret_cast<const float*>(x[q]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              a[e] += f[e];
+              if constexpr (C::DUAL) u[e] += f[8 + e];
+            }
+          }
+        }
+        finish8<C::EPI>(p, problem, (int64_t)tm * 128 + rr, (int64_t)tn * C::OUTC + c, sa, su, a, u);
       }
       cluster_sync();                              // the partials stay until every CTA has read them
     }
@@ -674,12 +978,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) tile_kernel(const __grid_consta
 
 template <class C>
 kq_status launch(const char* what, const Maps& maps, const Params& p, int grid, cudaStream_t st) {
+  // shorter A boxes make shorter stages; the last stage's MMAs still read 128 rows from its A on
+  const int smem = C::SMEM - (C::STAGES - 1) * (128 - p.a_rows) * 128;
   // the attribute belongs to the device: set on every call, as the current device may change
   KQ_TRY(cuda_check(cudaFuncSetAttribute(tile_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM), what));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
