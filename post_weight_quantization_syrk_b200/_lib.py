@@ -568,38 +568,63 @@ def kq_solver_timing(enable):
 
 
 # ------------------------------------- microscaled 4-bit floating point
+#
+# These calls take microseconds on the device, so their wrappers keep the host's
+# share small: integer device and stream handles instead of objects, one
+# allocation per result.
 
 _DTYPES = {torch.float32: KQ_F32, torch.bfloat16: KQ_BF16}
 
 
-def _on_device(*tensors):
-    """The tensors lie on one CUDA device, the current one (whose stream the work goes to)."""
-    dev = tensors[0].device
-    if not tensors[0].is_cuda or dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors must lie on the current CUDA device, got {dev}")
-    for t in tensors[1:]:
-        if t is not None and t.device != dev:
+def _device(first, *others):
+    """Index of the CUDA device that holds all the tensors: the current one,
+    whose stream the work goes to."""
+    dev = first.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors must lie on the current CUDA device, got {first.device}")
+    for t in others:
+        if t is not None and t.get_device() != dev:
             raise ValueError("tensors must lie on one device")
+    return dev
+
+
+def _handle(stream, dev):
+    """The CUDA stream handle as an integer: of `stream`, or the device's current one."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _rows(t, dtype, name):
+    """_mat for tensors whose device _device checks."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D row-major tensor (unit column stride)")
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError(f"{name} must be a 2-D row-major tensor (unit column stride)")
+    return ld if rows > 1 else max(cols, ld)
 
 
 def _dtype_code(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
     return code
 
 
-def _out(t, shape, dtype, device, name, multiple=1):
+def _out(t, rows, cols, dtype, like, name, multiple=1):
     """An output matrix and its leading dimension: checked, or a new one whose
     rows lie a multiple of `multiple` elements apart."""
     if t is None:
-        rows, cols = shape
         ld = -(-cols // multiple) * multiple
-        t = torch.empty((rows, ld), dtype=dtype, device=device)
+        t = like.new_empty((rows, ld), dtype=dtype)
         return (t if ld == cols else t[:, :cols]), ld
-    ld = _mat(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}")
+    ld = _rows(t, dtype, name)
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be {[rows, cols]}")
     return t, ld
 
 
@@ -614,22 +639,58 @@ class Fp4Matrix:
         ld = _mat(codes, torch.uint8, "codes")
         if codes.shape[0] != rows or codes.shape[1] < -(-cols // 32) * 16:
             raise ValueError("codes must be [rows, >= ceil(cols / 32) * 16]")
-        if codes.shape[0] <= 1:
+        if rows <= 1:
             ld = -(-ld // 16) * 16      # a single row: the distance to the next is not used
         if scales.dtype != torch.uint8 or not scales.is_contiguous() or \
                 scales.numel() < kq_fp4_scale_bytes(rows, cols, format):
             raise ValueError("scales must be contiguous uint8 with kq_fp4_scale_bytes(rows, cols, format) elements")
-        if gscale is not None and (gscale.dtype != torch.float32 or gscale.numel() != 1):
-            raise TypeError("gscale must be one float32 element")
         for t in (scales, gscale):
             if t is not None and t.device != codes.device:
                 raise ValueError("codes, scales and gscale must lie on one device")
-        self.rows, self.cols, self.format = rows, cols, format
-        self.codes, self.scales, self.gscale = codes, scales, gscale
-        self.device = codes.device
-        self.is_cuda = codes.is_cuda
-        self.c = kq_fp4(rows, cols, ld, format, codes.data_ptr(), scales.data_ptr(),
-                        0 if gscale is None else gscale.data_ptr())
+        self._codes, self._scales = codes, scales
+        self._set(rows, cols, format, ld, codes.data_ptr(), scales.data_ptr(), gscale, codes.get_device())
+
+    @classmethod
+    def empty(cls, rows, cols, format, like, gscale=None):
+        """A matrix to be filled, on the device of the tensor `like`: codes and scales in one allocation."""
+        self = cls.__new__(cls)
+        ld = -(-cols // 32) * 16
+        nbytes = -(-rows // 128) * -(-cols // (128 if format == KQ_FP4_MX else 64)) * 512
+        self._buf = like.new_empty(rows * ld + nbytes, dtype=torch.uint8)
+        self._codes = self._scales = None
+        base = self._buf.data_ptr()
+        self._set(rows, cols, format, ld, base, base + rows * ld, gscale, like.get_device())
+        return self
+
+    def _set(self, rows, cols, format, ld, codes, scales, gscale, dev):
+        if gscale is not None and (gscale.dtype != torch.float32 or gscale.numel() != 1):
+            raise TypeError("gscale must be one float32 element")
+        self.rows, self.cols, self.format, self.ld = rows, cols, format, ld
+        self.gscale, self._dev = gscale, dev
+        self.c = kq_fp4(rows, cols, ld, format, codes, scales, None if gscale is None else gscale.data_ptr())
+        self._ref = ctypes.byref(self.c)
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._codes = self._buf[:self.rows * self.ld].view(self.rows, self.ld)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._scales = self._buf[self.rows * self.ld:]
+        return self._scales
+
+    @property
+    def device(self):
+        return (self._codes if self._codes is not None else self._buf).device
+
+    def get_device(self):
+        return self._dev
+
+    def _like(self):
+        return self._codes if self._codes is not None else self._buf
 
 
 def kq_fp4_scale_bytes(rows: int, cols: int, format: int) -> int:
@@ -640,24 +701,28 @@ def kq_fp4_quantize(M, format, gscale=None, M_hat=None, out=None, info=None, str
     """M (float32 or bf16 [rows, cols]) to a microscaled 4-bit matrix; M_hat
     float32 [rows, cols]: the values its codes stand for."""
     dtype = _dtype_code(M, "M")
-    ldm = _mat(M, M.dtype, "M")
+    ldm = _rows(M, M.dtype, "M")
     rows, cols = M.shape
-    _on_device(M, gscale, M_hat, info)
+    dev = _device(M, gscale, M_hat, out, info)
     if out is None:
-        codes = torch.empty((rows, -(-cols // 32) * 16), dtype=torch.uint8, device=M.device)
-        scales = torch.empty(kq_fp4_scale_bytes(rows, cols, format), dtype=torch.uint8, device=M.device)
-        out = Fp4Matrix(rows, cols, format, codes, scales, gscale)
+        if format != KQ_FP4_MX and format != KQ_FP4_NV:
+            raise ValueError("format must be KQ_FP4_MX or KQ_FP4_NV")
+        if cols < 1:
+            raise ValueError("M needs at least one column")
+        out = Fp4Matrix.empty(rows, cols, format, M, gscale)
     else:
-        _on_device(M, out)
-        if (out.rows, out.cols, out.format) != (rows, cols, int(format)):
+        if (out.rows, out.cols, out.format) != (rows, cols, format):
             raise ValueError("out has another shape or format")
         if gscale is not None and (out.gscale is None or out.gscale.data_ptr() != gscale.data_ptr()):
             raise ValueError("out has another gscale")
-    ldh = cols if M_hat is None else _out(M_hat, (rows, cols), torch.float32, M.device, "M_hat")[1]
+    hat, ldh = None, cols
+    if M_hat is not None:
+        ldh = _out(M_hat, rows, cols, torch.float32, M, "M_hat")[1]
+        hat = M_hat.data_ptr()
     if info is None:
         info = new_info(M.device)
-    _check(load().kq_fp4_quantize(M.data_ptr(), dtype, ldm, out.c, None if M_hat is None else M_hat.data_ptr(), ldh,
-                                  info.data_ptr(), _stream(stream)), "kq_fp4_quantize")
+    _check(load().kq_fp4_quantize(M.data_ptr(), dtype, ldm, out._ref, hat, ldh, info.data_ptr(), _handle(stream, dev)),
+           "kq_fp4_quantize")
     return out
 
 
@@ -665,13 +730,14 @@ def kq_fp4_gemm(A, B, Y=None, dtype=torch.bfloat16, info=None, stream=None):
     """Y [A.rows, B.rows] = A B^T, bf16 or float32."""
     if Y is not None:
         dtype = Y.dtype
-    if dtype not in _DTYPES:
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise TypeError("Y must be float32 or bfloat16")
-    _on_device(A, B, Y, info)
-    Y, ldy = _out(Y, (A.rows, B.rows), dtype, A.device, "Y", 8)
+    dev = _device(A, B, Y, info)
+    Y, ldy = _out(Y, A.rows, B.rows, dtype, A._like(), "Y", 8)
     if info is None:
         info = new_info(A.device)
-    _check(load().kq_fp4_gemm(A.c, B.c, Y.data_ptr(), _DTYPES[dtype], ldy, info.data_ptr(), _stream(stream)),
+    _check(load().kq_fp4_gemm(A._ref, B._ref, Y.data_ptr(), code, ldy, info.data_ptr(), _handle(stream, dev)),
            "kq_fp4_gemm")
     return Y
 
@@ -679,39 +745,41 @@ def kq_fp4_gemm(A, B, Y=None, dtype=torch.bfloat16, info=None, stream=None):
 def kq_fp4_matvec(W, X, Y=None, stream=None):
     """Y [batch, W.rows] = X W^T for unquantized X [batch (1..8), W.cols], in X's dtype."""
     dtype = _dtype_code(X, "X")
-    ldx = _mat(X, X.dtype, "X")
-    _on_device(W, X, Y)
-    batch = X.shape[0]
-    if X.shape[1] != W.cols:
+    ldx = _rows(X, X.dtype, "X")
+    dev = _device(X, W, Y)
+    batch, cols = X.shape
+    if cols != W.cols:
         raise ValueError("X must be [batch, W.cols]")
-    Y, ldy = _out(Y, (batch, W.rows), X.dtype, X.device, "Y")
-    _check(load().kq_fp4_matvec(W.c, X.data_ptr(), dtype, ldx, batch, Y.data_ptr(), ldy, _stream(stream)),
+    Y, ldy = _out(Y, batch, W.rows, X.dtype, X, "Y")
+    _check(load().kq_fp4_matvec(W._ref, X.data_ptr(), dtype, ldx, batch, Y.data_ptr(), ldy, _handle(stream, dev)),
            "kq_fp4_matvec")
     return Y
 
 
 def kq_fp4_gated_ffn(X, W_gate, W_up, act, H=None, info=None, stream=None):
     """H [X.rows, f] bf16 = act(X W_gate^T) * (X W_up^T) over 4-bit X and weights [f, d]."""
-    _on_device(X, W_gate, W_up, H, info)
-    H, ldh = _out(H, (X.rows, W_gate.rows), torch.bfloat16, X.device, "H", 8)
+    dev = _device(X, W_gate, W_up, H, info)
+    H, ldh = _out(H, X.rows, W_gate.rows, torch.bfloat16, X._like(), "H", 8)
     if info is None:
         info = new_info(X.device)
-    _check(load().kq_fp4_gated_ffn(X.c, W_gate.c, W_up.c, int(act), H.data_ptr(), ldh, info.data_ptr(),
-                                   _stream(stream)), "kq_fp4_gated_ffn")
+    _check(load().kq_fp4_gated_ffn(X._ref, W_gate._ref, W_up._ref, act, H.data_ptr(), ldh, info.data_ptr(),
+                                   _handle(stream, dev)), "kq_fp4_gated_ffn")
     return H
 
 
 # ------------------------------------- gated feed-forward block, bf16
 
-def _tma_mat(t, name):
+def _tma_rows(t, name):
     """Leading dimension of a bf16 matrix that a kernel reads by TMA."""
-    ld = _mat(t, torch.bfloat16, name)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    ld = _rows(t, torch.bfloat16, name)
     return -(-ld // 8) * 8 if t.shape[0] <= 1 else ld     # a single row: the distance to the next is not used
 
 
 def _gated_weights(X, W_gate, W_up):
-    ldw = _tma_mat(W_gate, "W_gate")
-    if W_up.shape != W_gate.shape or _tma_mat(W_up, "W_up") != ldw:
+    ldw = _tma_rows(W_gate, "W_gate")
+    if W_up.shape != W_gate.shape or _tma_rows(W_up, "W_up") != ldw:
         raise ValueError("W_gate and W_up need the same shape and leading dimension")
     if W_gate.shape[1] != X.shape[1]:
         raise ValueError("X [tokens, d], weights [f, d]")
@@ -720,14 +788,14 @@ def _gated_weights(X, W_gate, W_up):
 
 def kq_gated_ffn(X, W_gate, W_up, act, H=None, info=None, stream=None):
     """H [tokens, f] = act(X W_gate^T) * (X W_up^T), all bf16."""
-    ldx, ldw = _tma_mat(X, "X"), _gated_weights(X, W_gate, W_up)
-    _on_device(X, W_gate, W_up, H, info)
+    ldx, ldw = _tma_rows(X, "X"), _gated_weights(X, W_gate, W_up)
+    dev = _device(X, W_gate, W_up, H, info)
     (tokens, d), f = X.shape, W_gate.shape[0]
-    H, ldh = _out(H, (tokens, f), torch.bfloat16, X.device, "H", 8)
+    H, ldh = _out(H, tokens, f, torch.bfloat16, X, "H", 8)
     if info is None:
         info = new_info(X.device)
-    _check(load().kq_gated_ffn(X.data_ptr(), tokens, d, ldx, W_gate.data_ptr(), W_up.data_ptr(), f, ldw, int(act),
-                               H.data_ptr(), ldh, info.data_ptr(), _stream(stream)), "kq_gated_ffn")
+    _check(load().kq_gated_ffn(X.data_ptr(), tokens, d, ldx, W_gate.data_ptr(), W_up.data_ptr(), f, ldw, act,
+                               H.data_ptr(), ldh, info.data_ptr(), _handle(stream, dev)), "kq_gated_ffn")
     return H
 
 
@@ -735,33 +803,33 @@ def kq_gated_ffn_backward(X, W_gate, W_up, dH, act, dG=None, dU=None, H=None, dX
                           need_dX=True, need_dW=True, info=None, stream=None):
     """(dG, dU, dX, dW_gate, dW_up) of kq_gated_ffn, all bf16; H (when given)
     gets the block's output.  need_dX / need_dW False: None in those places."""
-    ldx, ldw = _tma_mat(X, "X"), _gated_weights(X, W_gate, W_up)
-    lddh = _mat(dH, torch.bfloat16, "dH")
-    _on_device(X, W_gate, W_up, dH, dG, dU, H, dX, dW_gate, dW_up, info)
+    ldx, ldw = _tma_rows(X, "X"), _gated_weights(X, W_gate, W_up)
+    lddh = _rows(dH, torch.bfloat16, "dH")
+    dev = _device(X, W_gate, W_up, dH, dG, dU, H, dX, dW_gate, dW_up, info)
     (tokens, d), f = X.shape, W_gate.shape[0]
-    if tuple(dH.shape) != (tokens, f):
+    if dH.shape != (tokens, f):
         raise ValueError("dH must be [tokens, f]")
-    bf, dev = torch.bfloat16, X.device
-    dG, ldg = _out(dG, (tokens, f), bf, dev, "dG", 8)
-    dU, ldu = _out(dU, (tokens, f), bf, dev, "dU", 8)
+    bf = torch.bfloat16
+    dG, ldg = _out(dG, tokens, f, bf, X, "dG", 8)
+    dU, ldu = _out(dU, tokens, f, bf, X, "dU", 8)
     if tokens <= 1:
         ldg = ldu = -(-max(ldg, ldu) // 8) * 8
     if ldg != ldu:
         raise ValueError("dG and dU need the same leading dimension")
-    ldh = f if H is None else _out(H, (tokens, f), bf, dev, "H")[1]
+    ldh = f if H is None else _out(H, tokens, f, bf, X, "H")[1]
     lddx = lddw = d
     if need_dX:
-        dX, lddx = _out(dX, (tokens, d), bf, dev, "dX", 8)
+        dX, lddx = _out(dX, tokens, d, bf, X, "dX", 8)
     if need_dW:
-        dW_gate, lddw = _out(dW_gate, (f, d), bf, dev, "dW_gate", 8)
-        dW_up, ld2 = _out(dW_up, (f, d), bf, dev, "dW_up", 8)
+        dW_gate, lddw = _out(dW_gate, f, d, bf, X, "dW_gate", 8)
+        dW_up, ld2 = _out(dW_up, f, d, bf, X, "dW_up", 8)
         if ld2 != lddw:
             raise ValueError("dW_gate and dW_up need the same leading dimension")
     if info is None:
-        info = new_info(dev)
+        info = new_info(X.device)
     _check(load().kq_gated_ffn_backward(
-        X.data_ptr(), tokens, d, ldx, W_gate.data_ptr(), W_up.data_ptr(), f, ldw, int(act), dH.data_ptr(), lddh,
+        X.data_ptr(), tokens, d, ldx, W_gate.data_ptr(), W_up.data_ptr(), f, ldw, act, dH.data_ptr(), lddh,
         dG.data_ptr(), dU.data_ptr(), ldg, None if H is None else H.data_ptr(), ldh,
         dX.data_ptr() if need_dX else None, lddx, dW_gate.data_ptr() if need_dW else None,
-        dW_up.data_ptr() if need_dW else None, lddw, info.data_ptr(), _stream(stream)), "kq_gated_ffn_backward")
+        dW_up.data_ptr() if need_dW else None, lddw, info.data_ptr(), _handle(stream, dev)), "kq_gated_ffn_backward")
     return dG, dU, (dX if need_dX else None), (dW_gate if need_dW else None), (dW_up if need_dW else None)

@@ -23,34 +23,86 @@ __device__ __forceinline__ float as_float<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// Eight elements from column c of a row, zeros past `cols`.
-__device__ __forceinline__ void load8(const float* row, int64_t c, int64_t cols, bool vec, float (&v)[8]) {
-  if (vec && c + 8 <= cols) {
-    const float4 a = *reinterpret_cast<const float4*>(row + c), b = *reinterpret_cast<const float4*>(row + c + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? row[c + i] : 0.f;
-  }
+// 32 bytes in one access.
+__device__ __forceinline__ void ld32bytes(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* row, int64_t c, int64_t cols, bool vec, float (&v)[8]) {
-  if (vec && c + 8 <= cols) {
-    const uint4 q = *reinterpret_cast<const uint4*>(row + c);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+__device__ __forceinline__ void st32bytes(void* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]),
+               "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+// How rows can be accessed: 32 bytes at a time, 16, or element by element.
+enum { ACCESS_ANY = 0, ACCESS_16 = 1, ACCESS_32 = 2 };
+int access_of(const void* p, int64_t ld_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(p) | (uintptr_t)ld_bytes;
+  return x % 32 == 0 ? ACCESS_32 : (x % 16 == 0 ? ACCESS_16 : ACCESS_ANY);
+}
+
+// Sixteen elements from column c of an aligned row as their bit patterns (W
+// words: fp32 one per word, bf16 two), zeros past `cols`.
+template <typename T, int W>
+__device__ __forceinline__ void load16(const T* row, int c, int cols, int access, uint32_t (&w)[W]) {
+  if (c + 16 <= cols) {
+    const T* src = row + c;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < W; i += 8) {
+      if (access == ACCESS_32) {
+        ld32bytes(reinterpret_cast<const uint32_t*>(src) + i, *reinterpret_cast<uint32_t(*)[8]>(w + i));
+      } else {
+        const uint4 a = reinterpret_cast<const uint4*>(src)[i / 4], b = reinterpret_cast<const uint4*>(src)[i / 4 + 1];
+        w[i] = a.x; w[i + 1] = a.y; w[i + 2] = a.z; w[i + 3] = a.w;
+        w[i + 4] = b.x; w[i + 5] = b.y; w[i + 6] = b.z; w[i + 7] = b.w;
+      }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? __bfloat162float(row[c + i]) : 0.f;
+    for (int i = 0; i < W; ++i) w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (c + i >= cols) continue;
+      if constexpr (sizeof(T) == 4)
+        w[i] = __float_as_uint(row[c + i]);
+      else
+        w[i / 2] |= (uint32_t)__bfloat16_as_ushort(row[c + i]) << (16 * (i & 1));
+    }
   }
 }
 
+// Rows that are not 16-byte aligned go through shared memory: the lanes of a row
+// take neighbouring elements of it, so that global accesses stay coalesced, and
+// lane l's sixteen words lie 20 l words into the warp's buffer (no bank conflicts
+// at 16 bytes per lane).
+constexpr int kStageWords = 32 * 20;
+__device__ __forceinline__ int stage_at(int first_lane, int e) { return 20 * (first_lane + e / 16) + e % 16; }
+
+// Largest magnitude of the 16, as an fp32 bit pattern: non-negative floats order
+// as integers, and NaN and Inf lie on top.
+__device__ __forceinline__ uint32_t top_of(const uint32_t (&w)[16]) {
+  uint32_t t = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) t = max(t, w[i] & 0x7fffffffu);
+  return t;
+}
+__device__ __forceinline__ uint32_t top_of(const uint32_t (&w)[8]) {
+  uint32_t t = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t a = w[i] & 0x7fff7fffu;
+    asm("max.u16x2 %0, %0, %1;" : "+r"(t) : "r"(a));
+  }
+  return max(t << 16, t & 0xffff0000u);
+}
+__device__ __forceinline__ float element(const uint32_t (&w)[16], int i) { return __uint_as_float(w[i]); }
+__device__ __forceinline__ float element(const uint32_t (&w)[8], int i) {
+  return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+}
+
 // Eight values to eight codes: round to nearest even, saturating at 6.
-__device__ __forceinline__ uint32_t encode8(const float (&q)[8]) {
+__device__ __forceinline__ uint32_t encode8(const float* q) {
   uint32_t w;
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -65,36 +117,42 @@ __device__ __forceinline__ uint32_t encode8(const float (&q)[8]) {
 
 // The value of code k of a word.
 __device__ __forceinline__ float decode1(uint32_t w, int k) {
-  const uint32_t c = (w >> (4 * k)) & 15u, m = c & 7u;
+  const uint32_t c = w >> (4 * k);
   // e2m1 as the top bits of an fp32 with exponent bias 127 - 126: exact, subnormal included
-  const float v = __uint_as_float(m << 22) * 0x1p126f;
-  return c & 8u ? -v : v;
+  return __uint_as_float(((c & 7u) << 22) | ((c & 8u) << 28)) * 0x1p126f;
 }
 
 struct QuantParams {
-  int64_t rows, cols, ldm, ldc, ldh;
-  int64_t chunks;       // 256-column pieces of a row, the scale tiles' padding included
-  int64_t units;        // (rows rounded up to 128) / R * chunks
-  int64_t kat;          // scale tiles along a row
+  int64_t rows, ldm, ldc, ldh;
+  int cols, kat;        // kat: scale tiles along a row
   const void* M;
   const float* g;
   uint8_t* codes;
   uint8_t* scales;
   float* M_hat;
-  int m_vec, h_vec;
+  int m_access, h_access;
   int32_t* info;
 };
 
-// One warp per 256 columns of R rows, eight columns per lane (so a lane's loads,
-// its 4 bytes of codes and its dequantized values are contiguous across the
-// warp); the R rows' loads are in flight together.  A block is 4 lanes (32
-// columns) or 2 (16): its amax is 2 or 1 shuffles away, and every fourth block's
-// lanes write 4 scale bytes as one word.  Bound by memory: one read of M, one
-// write of codes and scales (and of M_hat).
-template <typename T, int FMT, int R>
-__global__ void __launch_bounds__(256) quantize_kernel(const QuantParams p) {
-  constexpr int LANES = block_of(FMT) / 8;        // lanes per block
+// Sixteen columns per lane: a 16-column block is a lane's own, a 32-column one
+// two lanes'; four blocks' scale bytes leave as one word.  A warp takes 512
+// columns of a row (ROW_LANES 32), or 128 of 4 rows (8) where rows are short,
+// two such pieces with their loads in flight together.  The grid covers the scale
+// tiles' padding (rows to 128, blocks to 4), whose bytes are zeros.  Bound by
+// memory: one read of M, one write of codes and scales (and of M_hat).
+template <typename T, int FMT, int ROW_LANES>
+__global__ void __launch_bounds__(256, 4) quantize_kernel(const QuantParams p) {
+  constexpr int R = 2;                            // pieces of a warp
+  constexpr int LANES = block_of(FMT) / 16;       // lanes per block
+  constexpr int W = 16 * sizeof(T) / 4;           // words of 16 elements
   const int lane = threadIdx.x % 32;
+  constexpr int per = 32 / ROW_LANES;             // rows of a piece
+  const int64_t r0 = ((int64_t)blockIdx.x * 8 + threadIdx.x / 32) * (R * per) + lane / ROW_LANES;
+  const int c = ((int)blockIdx.y * ROW_LANES + lane % ROW_LANES) * 16;
+  const int padded = (p.cols + 31) / 32 * 32;
+  const int kb = c / block_of(FMT);
+  kq::pdl_wait();
+  kq::pdl_trigger();
   float g = 1.f, g6 = 6.f;
   bool g_ok = true;
   if (FMT == KQ_FP4_NV) {
@@ -102,88 +160,131 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantParams p) {
     g_ok = g > 0.f && isfinite(g);
     g6 = 6.f * g;
   }
-  const int64_t padded = (p.cols + 31) / 32 * 32;
-  for (int64_t unit = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; unit < p.units; unit += (int64_t)gridDim.x * 8) {
-    const int64_t r0 = unit / p.chunks * R, c = unit % p.chunks * 256 + 8 * lane;
-    float v[R][8];
+  __shared__ __align__(16) uint32_t stage_mem[8][kStageWords];
+  uint32_t* stage = stage_mem[threadIdx.x / 32];
+  const int row_lane = lane % ROW_LANES, first_lane = lane - row_lane, c_row = c - 16 * row_lane;
+  uint32_t v[R][W];
+  if (p.m_access == ACCESS_ANY) {
+    uint32_t e[R][16];
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      if (r0 + k < p.rows && c < p.cols) {
-        load8(static_cast<const T*>(p.M) + (r0 + k) * p.ldm, c, p.cols, p.m_vec, v[k]);
-      } else {
+      const int64_t r = r0 + k * per;
+      const T* row = static_cast<const T*>(p.M) + r * p.ldm + c_row + row_lane;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
-      }
+      for (int i = 0; i < 16; ++i)
+        e[k][i] = r < p.rows && c_row + row_lane + i * ROW_LANES < p.cols ? __float_as_uint(as_float(row[i * ROW_LANES])) : 0u;
     }
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      const int64_t r = r0 + k;
-      // amax as bits: non-negative floats order as integers, and NaN and Inf lie on top
-      uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[k][i]) & 0x7fffffffu);
+      for (int i = 0; i < 16; ++i) stage[stage_at(first_lane, i * ROW_LANES + row_lane)] = e[k][i];
+      __syncwarp();
 #pragma unroll
-      for (int o = 1; o < LANES; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float amax = __uint_as_float(top);
-      const bool bad = top >= 0x7f800000u || !g_ok;
-      uint32_t byte;
-      float d, q[8];
-      if (FMT == KQ_FP4_MX) {
-        // 2^(floor(log2 amax) - 2) from the exponent field; at least 2^-127
-        const int field = max((int)(top >> 23) - 2, 0);
-        byte = bad ? 0xffu : (uint32_t)field;
-        d = field ? __uint_as_float((uint32_t)field << 23) : 0x1p-127f;
-        const float inv = __uint_as_float((uint32_t)(254 - field) << 23);   // 1 / d, a power of two
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = v[k][i] * inv;
-      } else {
-        const float t = fminf(__fdiv_rn(amax, g6), 448.f);
-        uint16_t pair;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pair) : "f"(0.f), "f"(t));
-        byte = bad ? 0x7fu : (uint32_t)(pair & 0xff);
-        d = kq::fp4::e4m3_value(byte) * g;
-        // v / d rounded to fp32.  With the reciprocal r rounded once per block,
-        // q0 = v r is within 2 ulp and fma(v - q0 d, r, q0) is the rounded
-        // quotient (Markstein's correction step: the residual is exact in an
-        // fma); a divide per element would bound the kernel.  Outside the
-        // range where the residual is exact, the divide.
-        if (d >= 0x1p-90f && d <= 0x1p90f && amax <= 1024.f * d) {
-          const float r = __frcp_rn(d);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float q0 = v[k][i] * r;
-            q[i] = fmaf(fmaf(-q0, d, v[k][i]), r, q0);
-          }
+      for (int i = 0; i < 16; i += 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(stage + 20 * lane + i);
+        if constexpr (W == 16) {
+          v[k][i] = x.x; v[k][i + 1] = x.y; v[k][i + 2] = x.z; v[k][i + 3] = x.w;
         } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) q[i] = d > 0.f ? __fdiv_rn(v[k][i], d) : 0.f;
+          v[k][i / 2] = __byte_perm(x.x, x.y, 0x7632);
+          v[k][i / 2 + 1] = __byte_perm(x.z, x.w, 0x7632);
         }
       }
-      uint32_t w = bad ? 0u : encode8(q);
-      if (bad && r < p.rows && c < p.cols) kq::report(p.info, g_ok ? KQ_ERR_NONFINITE : KQ_ERR_INVALID_ARG, r);
-      if (r < p.rows && c < padded) *reinterpret_cast<uint32_t*>(p.codes + r * p.ldc + c / 2) = w;
-      // four blocks' bytes as one word, written by the first lane of the four
-      uint32_t word = byte << (8 * ((lane / LANES) & 3));
+      __syncwarp();
+    }
+  } else {
 #pragma unroll
-      for (int o = LANES; o < 4 * LANES; o *= 2) word |= __shfl_xor_sync(0xffffffffu, word, o);
-      const int64_t kb = c / block_of(FMT);
-      // a block past the row's end is a block of zeros: byte 0
-      if (lane % (4 * LANES) == 0 && kb / 4 < p.kat)
-        *reinterpret_cast<uint32_t*>(p.scales + kq::fp4::scale_offset(r, kb, p.kat)) = r < p.rows ? word : 0u;
-      if (p.M_hat && r < p.rows && c < p.cols) {
-        if (bad) d = __uint_as_float(0x7fc00000u);
-        float* dst = p.M_hat + r * p.ldh + c;
-        float h[8];
+    for (int k = 0; k < R; ++k) {
+      const int64_t r = r0 + k * per;
+      if (r < p.rows && c < p.cols) {
+        load16(static_cast<const T*>(p.M) + r * p.ldm, c, p.cols, p.m_access, v[k]);
+      } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = decode1(w, i) * d;
-        if (p.h_vec && c + 8 <= p.cols) {
-          reinterpret_cast<float4*>(dst)[0] = make_float4(h[0], h[1], h[2], h[3]);
-          reinterpret_cast<float4*>(dst)[1] = make_float4(h[4], h[5], h[6], h[7]);
+        for (int i = 0; i < W; ++i) v[k][i] = 0;
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const int64_t r = r0 + k * per;
+    uint32_t top = top_of(v[k]);
+    if (LANES == 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    const bool bad = top >= 0x7f800000u || !g_ok;
+    uint32_t byte;
+    float d, q[16];
+    if (FMT == KQ_FP4_MX) {
+      // 2^(floor(log2 amax) - 2) from the exponent field; at least 2^-127
+      const int field = max((int)(top >> 23) - 2, 0);
+      byte = bad ? 0xffu : (uint32_t)field;
+      d = field ? __uint_as_float((uint32_t)field << 23) : 0x1p-127f;
+      const float inv = __uint_as_float((uint32_t)(254 - field) << 23);   // 1 / d, a power of two
+#pragma unroll
+      for (int i = 0; i < 16; ++i) q[i] = element(v[k], i) * inv;
+    } else {
+      const float amax = __uint_as_float(top);
+      const float t = fminf(__fdiv_rn(amax, g6), 448.f);
+      uint16_t pair;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pair) : "f"(0.f), "f"(t));
+      byte = bad ? 0x7fu : (uint32_t)(pair & 0xff);
+      d = kq::fp4::e4m3_value(byte) * g;
+      // v / d rounded to fp32.  With the reciprocal r rounded once per block,
+      // q0 = v r is within 2 ulp and fma(v - q0 d, r, q0) is the rounded
+      // quotient (Markstein's correction step: the residual is exact in an
+      // fma); a divide per element would bound the kernel.  Outside the
+      // range where the residual is exact, the divide.
+      if (d >= 0x1p-90f && d <= 0x1p90f && amax <= 1024.f * d) {
+        const float r = __frcp_rn(d);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float x = element(v[k], i), q0 = x * r;
+          q[i] = fmaf(fmaf(-q0, d, x), r, q0);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q[i] = d > 0.f ? __fdiv_rn(element(v[k], i), d) : 0.f;
+      }
+    }
+    uint32_t w0 = bad ? 0u : encode8(q), w1 = bad ? 0u : encode8(q + 8);
+    if (bad && r < p.rows && c < p.cols) kq::report(p.info, g_ok ? KQ_ERR_NONFINITE : KQ_ERR_INVALID_ARG, r);
+    if (r < p.rows && c < padded) *reinterpret_cast<uint2*>(p.codes + r * p.ldc + c / 2) = make_uint2(w0, w1);
+    // four blocks' bytes as one word, written by the first lane of the four
+    uint32_t word = byte << (8 * ((lane / LANES) & 3));
+#pragma unroll
+    for (int o = LANES; o < 4 * LANES; o *= 2) word |= __shfl_xor_sync(0xffffffffu, word, o);
+    // a row past the end has zero scales (its values are zeros: MX byte 0 too)
+    if (lane % (4 * LANES) == 0 && kb / 4 < p.kat && r < (p.rows + 127) / 128 * 128)
+      *reinterpret_cast<uint32_t*>(p.scales + kq::fp4::scale_offset(r, kb, p.kat)) = r < p.rows ? word : 0u;
+    if (p.M_hat) {
+      if (bad) d = __uint_as_float(0x7fc00000u);
+      float h[16];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        h[i] = decode1(w0, i) * d;
+        h[i + 8] = decode1(w1, i) * d;
+      }
+      float* row = p.M_hat + r * p.ldh;
+      if (p.h_access == ACCESS_ANY) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<float4*>(stage + 20 * lane + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int e = i * ROW_LANES + row_lane;
+          if (r < p.rows && c_row + e < p.cols) row[c_row + e] = __uint_as_float(stage[stage_at(first_lane, e)]);
+        }
+        __syncwarp();
+      } else if (r < p.rows && c + 16 <= p.cols) {
+        if (p.h_access == ACCESS_32) {
+          st32bytes(row + c, h);
+          st32bytes(row + c + 8, h + 8);
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (c + i < p.cols) dst[i] = h[i];
+          for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(row + c + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
         }
+      } else if (r < p.rows) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (c + i < p.cols) row[c + i] = h[i];
       }
     }
   }
@@ -320,6 +421,8 @@ __global__ void __launch_bounds__(kWarps * 32) matvec_kernel(const MatvecParams 
   const int64_t r0 = (int64_t)blockIdx.x * 16;
   const int64_t chunks = (p.d_in + 127) / 128, padded = (p.d_in + 31) / 32 * 32;
   const T* x = static_cast<const T*>(p.X) + (g < p.batch ? g : 0) * p.ldx;
+  kq::pdl_wait();
+  kq::pdl_trigger();
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   for (int64_t ch = warp; ch < chunks; ch += kWarps) {
     const int64_t k = 128 * ch + 32 * t;
@@ -387,20 +490,23 @@ __global__ void __launch_bounds__(kWarps * 32) matvec_kernel(const MatvecParams 
   }
 }
 
+template <typename T, int FMT, int ROW_LANES>
+kq_status launch_pieces(const QuantParams& p, cudaStream_t st) {
+  const dim3 grid((unsigned)kq::cdiv(kq::cdiv(p.rows, 128) * 128, 8 * 2 * (32 / ROW_LANES)),
+                  (unsigned)kq::cdiv((int64_t)p.kat * 4 * block_of(FMT), 16 * ROW_LANES));
+  return kq::launch_ex("kq_fp4_quantize", true, quantize_kernel<T, FMT, ROW_LANES>, grid, dim3(256), 0, st, p);
+}
+
 template <typename T, int FMT>
 kq_status launch_quantize(const QuantParams& p, cudaStream_t st) {
-  constexpr int R = 4;
-  QuantParams q = p;
-  q.units = kq::cdiv(p.rows, 128) * (128 / R) * p.chunks;
-  const int64_t grid = std::min<int64_t>(kq::cdiv(q.units, 8), 148 * 8);
-  quantize_kernel<T, FMT, R><<<(unsigned)grid, 256, 0, st>>>(q);
-  return kq::launch_check("kq_fp4_quantize");
+  // up to 384 columns, pieces of 128 leave fewer lanes idle than pieces of 512
+  return p.cols <= 384 ? launch_pieces<T, FMT, 8>(p, st) : launch_pieces<T, FMT, 32>(p, st);
 }
 
 template <typename T, int FMT>
 kq_status launch_matvec(const MatvecParams& p, cudaStream_t st) {
-  matvec_kernel<T, FMT><<<(unsigned)kq::cdiv(p.d_out, 16), kWarps * 32, 0, st>>>(p);
-  return kq::launch_check("kq_fp4_matvec");
+  return kq::launch_ex("kq_fp4_matvec", true, matvec_kernel<T, FMT>, dim3((unsigned)kq::cdiv(p.d_out, 16)), dim3(kWarps * 32), 0,
+                       st, p);
 }
 
 }  // namespace
@@ -427,19 +533,18 @@ extern "C" kq_status kq_fp4_quantize(const void* M, int dtype, int64_t ldm, cons
     return kq::fail(KQ_ERR_ALIGNMENT, "kq_fp4_quantize: M and M_hat aligned to their elements");
   QuantParams p = {};
   p.rows = Q->rows;
-  p.cols = Q->cols;
+  p.cols = (int)Q->cols;
   p.ldm = ldm;
   p.ldc = Q->ld;
   p.ldh = ldh;
-  p.kat = kq::fp4::scale_tiles(Q->cols, Q->format);
-  p.chunks = kq::cdiv(p.kat * 4 * block_of(Q->format), 256);
+  p.kat = (int)kq::fp4::scale_tiles(Q->cols, Q->format);
   p.M = M;
   p.g = Q->gscale;
   p.codes = Q->codes;
   p.scales = Q->scales;
   p.M_hat = M_hat;
-  p.m_vec = kq::aligned(M, 16) && (ldm * (int64_t)esize) % 16 == 0;
-  p.h_vec = kq::aligned(M_hat, 16) && ldh % 4 == 0;
+  p.m_access = access_of(M, ldm * (int64_t)esize);
+  p.h_access = access_of(M_hat, ldh * 4);
   p.info = info;
   cudaStream_t st = (cudaStream_t)stream;
   if (dtype == KQ_F32)

@@ -582,6 +582,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
   if (CG == 2 || ks > 1) cluster_sync();   // the other CTAs' barriers are ready too
   fence_after();
   const uint32_t tmem = *tmem_slot;
+  // what comes before overlaps the kernel ahead on the stream; no global memory so far
+  pdl_wait();
+  pdl_trigger();
   const uint32_t sf0 = tmem + C::NBUF * C::BN;
 
   // The scales of stages kb0 .. kb1 of a tile, by one of the four warps that write them.
@@ -987,13 +990,15 @@ kq_status launch(const char* what, const Maps& maps, const Params& p, int grid, 
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C::CG == 2 ? 2 : p.ks;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C::CG == 2 ? 2 : p.ks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = (C::CG == 2 || p.ks > 1) ? 1 : 0;
+  cfg.numAttrs = (C::CG == 2 || p.ks > 1) ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, tile_kernel<C>, maps, p);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();

@@ -154,7 +154,7 @@ def test_python_wrappers_check_their_tensors():
     with pytest.raises(TypeError):
         P.kq_fp4_quantize(x.half(), P.KQ_FP4_MX)
     with pytest.raises(ValueError, match="current CUDA device"):
-        K._on_device(x)
+        K._device(x)
     with pytest.raises(TypeError, match="CUDA tensor"):
         P.Fp4Matrix(4, 64, P.KQ_FP4_MX, torch.zeros((4, 32), dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8))
     with pytest.raises(ValueError, match="format"):
