@@ -298,13 +298,27 @@ __global__ void __launch_bounds__(256, 4) quantize_kernel(const QuantParams p) {
 // vectors enter as they are; fp32 vectors as three bf16 parts that sum to them
 // (24 bits), one MMA each.
 //
-// A warp takes 128 columns of 16 rows per step; lane (g, t) = (lane / 4, lane %
-// 4) holds 32 consecutive codes of rows g and g + 8 (16-byte loads).  The K
-// order inside an MMA is free as long as both operands share it: a register
-// pairs codes p and p + 4 of a word, which three logic operations bring to
-// bf16 position, and x is paired alike.  The warps of a CTA split K; their sums
-// are added in warp order through shared memory.
+// A warp takes 16 rows and goes through its share of K in steps of 128 columns:
+// lane (g, t) = (lane / 4, lane % 4) holds 32 consecutive codes of rows g and g +
+// 8 and 32 elements of vector g.  A lane's codes and scales arrive by asynchronous
+// copies in a ring of its own in shared memory, kDepth steps ahead: a step is 1 KB
+// per warp, and an SM needs some 40 KB in flight to draw its share of the memory
+// rate (with the next step alone in flight, in registers, a step took the 1 us of
+// a load).  The
+// K order inside an MMA is free as long as both operands share it: a register
+// pairs codes p and p + 4 of a word, which four logic operations bring to bf16
+// position, and x is paired alike.  Two arrangements:
+//  * bf16 vectors: the 8 warps of a CTA split K of the same 16 rows, each reading
+//    the x it needs.
+//  * fp32 vectors: splitting x into parts costs as much as decoding the codes of
+//    16 rows, and its 4 KB a step (8 vectors) four times their bytes.  So the 8
+//    warps of a CTA take 128 rows of the same columns, the parts are formed once
+//    per CTA in shared memory, and K is split over a cluster of up to 8 CTAs, whose
+//    sums meet in distributed shared memory.
+// Sums are added in a fixed order in both.
 constexpr int kWarps = 8;
+constexpr int kDepth = 4;         // steps of codes in flight (a power of two)
+constexpr int kStageSteps = 12;   // steps of x parts in shared memory at a time (72 KB)
 
 struct MatvecParams {
   const uint8_t* codes;
@@ -313,7 +327,7 @@ struct MatvecParams {
   int64_t d_out, d_in, ldc, kat;
   const void* X;
   int64_t ldx;
-  int x_vec, batch;
+  int x_vec, batch, ks;   // ks: CTAs along K (fp32)
   void* Y;
   int64_t ldy;
 };
@@ -339,13 +353,14 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// A block's scale as a bf16 pair to multiply spread() with: MX 2^k (after 2^126),
-// NV s 2^118 (the missing 2^8 is in the final factor; 448 2^126 would overflow).
+// A block's scale as a bf16 pair to multiply spread() with: MX 2^k, or 2^(k + 126)
+// where that fits; NV s 2^118 (the missing 2^8 is in the final factor; 448 2^126
+// would overflow).
 template <int FMT>
-__device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
+__device__ __forceinline__ uint32_t scale_pair(uint32_t byte, bool small) {
   uint32_t h;
   if (FMT == KQ_FP4_MX) {
-    h = byte == 0xffu ? 0x7fc0u : (byte ? byte << 7 : 0x0040u);
+    h = small ? (byte + 126u) << 7 : (byte == 0xffu ? 0x7fc0u : (byte ? byte << 7 : 0x0040u));
   } else {
     const float s = kq::fp4::e4m3_value(byte) * 0x1p118f;
     h = __float_as_uint(s) >> 16;
@@ -353,141 +368,252 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
   return h | (h << 16);
 }
 
+// Spread codes times their scale.  MX: with a scale up to 2 (`small`) its 2^126
+// fits in the factor, else 2^126 goes first.
 template <int FMT>
-__device__ __forceinline__ uint32_t weight(uint32_t spread_pair, uint32_t scale) {
-  if (FMT == KQ_FP4_MX) spread_pair = mul_bf16x2(spread_pair, 0x7e807e80u);   // 2^126
+__device__ __forceinline__ uint32_t weight(uint32_t spread_pair, uint32_t scale, bool small) {
+  if (FMT == KQ_FP4_MX && !small) spread_pair = mul_bf16x2(spread_pair, 0x7e807e80u);
   return mul_bf16x2(spread_pair, scale);
 }
 
-// 32 elements of a vector as pairs (8 j + p, 8 j + p + 4), in `PARTS` bf16 parts.
-template <typename T, int PARTS>
-__device__ __forceinline__ void load_x(const T* x, int64_t k, int64_t d_in, bool ok, bool vec, uint32_t (&b)[PARTS][16]) {
-  if constexpr (PARTS == 1) {
-    uint32_t w[16];
-    if (ok && vec && k + 32 <= d_in) {
+// 32 elements of a bf16 vector from column k as 16 words, zeros past d_in.
+__device__ __forceinline__ void load_x(const __nv_bfloat16* x, int64_t k, int64_t d_in, bool vec, uint32_t (&w)[16]) {
+  if (vec && k + 32 <= d_in) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 q = *reinterpret_cast<const uint4*>(x + k + 8 * i);
-        w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t lo = ok && k + 2 * i < d_in ? __bfloat16_as_ushort(x[k + 2 * i]) : 0u;
-        const uint32_t hi = ok && k + 2 * i + 1 < d_in ? __bfloat16_as_ushort(x[k + 2 * i + 1]) : 0u;
-        w[i] = lo | (hi << 16);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      b[0][4 * j] = __byte_perm(w[4 * j], w[4 * j + 2], 0x5410);
-      b[0][4 * j + 1] = __byte_perm(w[4 * j], w[4 * j + 2], 0x7632);
-      b[0][4 * j + 2] = __byte_perm(w[4 * j + 1], w[4 * j + 3], 0x5410);
-      b[0][4 * j + 3] = __byte_perm(w[4 * j + 1], w[4 * j + 3], 0x7632);
+    for (int i = 0; i < 4; ++i) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(x + k + 8 * i));
+      w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float v[8];
-      if (ok && vec && k + 8 * j + 8 <= d_in) {
-        const float4 q0 = *reinterpret_cast<const float4*>(x + k + 8 * j), q1 = *reinterpret_cast<const float4*>(x + k + 8 * j + 4);
-        v[0] = q0.x; v[1] = q0.y; v[2] = q0.z; v[3] = q0.w;
-        v[4] = q1.x; v[5] = q1.y; v[6] = q1.z; v[7] = q1.w;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = ok && k + 8 * j + i < d_in ? as_float(x[k + 8 * j + i]) : 0.f;
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float lo = v[q], hi = v[q + 4];
-#pragma unroll
-        for (int part = 0; part < PARTS; ++part) {
-          const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
-          b[part][4 * j + q] = *reinterpret_cast<const uint32_t*>(&r);
-          // the remainder is exact; an infinity (or a value that rounds to one) has none
-          lo = isfinite(__low2float(r)) ? lo - __low2float(r) : 0.f;
-          hi = isfinite(__high2float(r)) ? hi - __high2float(r) : 0.f;
-        }
-      }
-    }
+    for (int i = 0; i < 32; ++i)
+      if (k + i < d_in) w[i / 2] |= (uint32_t)__bfloat16_as_ushort(x[k + i]) << (16 * (i & 1));
   }
 }
 
+// Three bf16 parts of an fp32 value in the top halves of three words, by
+// truncation, 8 bits each: exact.  A value without a finite remainder (NaN, Inf)
+// is its first part alone.
+__device__ __forceinline__ void split3(float x, uint32_t (&part)[3]) {
+  part[0] = __float_as_uint(x);
+  if ((part[0] & 0x7f800000u) == 0x7f800000u) {
+    if (part[0] & 0x7fffffu) part[0] |= 0x400000u;   // a NaN whose top bits are zero stays one
+    part[1] = part[2] = 0;
+    return;
+  }
+  const float r1 = x - __uint_as_float(part[0] & 0xffff0000u);
+  part[1] = __float_as_uint(r1);
+  part[2] = __float_as_uint(r1 - __uint_as_float(part[1] & 0xffff0000u));
+}
+
+__device__ __forceinline__ float ld_cluster(const float* mine, uint32_t rank) {
+  uint32_t at;
+  float v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
 template <typename T, int FMT>
-__global__ void __launch_bounds__(kWarps * 32) matvec_kernel(const MatvecParams p) {
-  constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
-  __shared__ float sums[kWarps][16][8];
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 4 ? 3 : 4) matvec_kernel(const MatvecParams p) {
+  constexpr bool STAGED = sizeof(T) == 4;
+  constexpr int PARTS = STAGED ? 3 : 1;
+  constexpr int ROWS = STAGED ? 16 * kWarps : 16;   // rows of a CTA
+  constexpr int KW = STAGED ? 1 : kWarps;           // its warps along K
+  __shared__ float sums[KW][ROWS][8];
+  extern __shared__ uint4 xs[];   // [step][part][lane][4 pieces of 16 bytes], pieces swizzled by lane
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  const int64_t r0 = (int64_t)blockIdx.x * 16;
-  const int64_t chunks = (p.d_in + 127) / 128, padded = (p.d_in + 31) / 32 * 32;
-  const T* x = static_cast<const T*>(p.X) + (g < p.batch ? g : 0) * p.ldx;
+  const int rank = STAGED ? (int)blockIdx.x % p.ks : 0;
+  const int64_t row0 = (int64_t)(STAGED ? blockIdx.x / p.ks : blockIdx.x) * ROWS, r0 = row0 + (STAGED ? 16 * warp : 0);
+  // this warp's steps: first, first + KW, ... below last
+  const int steps = (int)((p.d_in + 127) / 128), padded = (int)((p.d_in + 31) / 32 * 32);
+  const int first = STAGED ? (int)((int64_t)steps * rank / p.ks) : warp;
+  const int last = STAGED ? (int)((int64_t)steps * (rank + 1) / p.ks) : steps;
+  // the lane's place in its two rows at step `first` (a row past the end reads the last one; never stored)
+  const uint8_t* codes[2];
+  const uint8_t* scales[2];   // the 4-byte word of four blocks that holds the lane's one (MX) or two (NV)
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t r = min(r0 + g + 8 * h, p.d_out - 1);
+    codes[h] = p.codes + r * p.ldc + 16 * t + 64 * (int64_t)first;
+    scales[h] = p.scales + kq::fp4::scale_offset(r, FMT == KQ_FP4_MX ? 4 * (int64_t)first : 8 * (int64_t)first + 4 * (t / 2), p.kat);
+  }
+  __shared__ uint4 code_ring[kDepth][2][kWarps * 32];
+  __shared__ uint32_t scale_ring[kDepth][2][kWarps * 32];
   kq::pdl_wait();
   kq::pdl_trigger();
+
+  // the copies of step `first + KW n` into slot n % kDepth; columns past the matrix are zeros
+  auto fetch = [&](int n) {
+    const int step = first + KW * n, slot = n & (kDepth - 1);
+    if (step < last) {
+      const int64_t ahead = (int64_t)KW * n;
+      const int bytes = 128 * step + 32 * t < padded ? 16 : 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t c = (uint32_t)__cvta_generic_to_shared(&code_ring[slot][h][threadIdx.x]);
+        const uint32_t z = (uint32_t)__cvta_generic_to_shared(&scale_ring[slot][h][threadIdx.x]);
+        const uint8_t* src = bytes ? codes[h] + 64 * ahead : p.codes;
+        const uint8_t* srs = bytes ? scales[h] + (FMT == KQ_FP4_MX ? 512 : 1024) * ahead : p.scales;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(c), "l"(src), "r"(bytes) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(z), "l"(srs), "r"(bytes / 4) : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t ch = warp; ch < chunks; ch += kWarps) {
-    const int64_t k = 128 * ch + 32 * t;
-    uint4 w[2];
+
+#pragma unroll
+  for (int n = 0; n < kDepth - 1; ++n) fetch(n);
+  int staged = 0;   // steps below this one are in shared memory
+  if (STAGED) {
+    // vectors past the batch: zeros, written once
+    for (int i = threadIdx.x; i < min(last - first, kStageSteps) * PARTS * 128; i += kWarps * 32)
+      if ((i / 4 % 32) / 4 >= p.batch) xs[i] = make_uint4(0, 0, 0, 0);
+    staged = first;
+  }
+  for (int step = first; step < last; step += KW) {
+    if (STAGED && step == staged) {
+      // the parts of the next steps' x: a thread takes (step, lane) slots of the batch
+      const int n = min(kStageSteps, last - step);
+      __syncthreads();
+      for (int i = threadIdx.x; i < n * 4 * p.batch; i += kWarps * 32) {
+        const int at = i / (4 * p.batch), slot = i % (4 * p.batch);   // slot: the lane it serves
+        const float* x = static_cast<const float*>(p.X) + (slot / 4) * p.ldx;
+        const int64_t k = 128 * (int64_t)(step + at) + 32 * (slot % 4);
+        float v[32];
+        if (p.x_vec && k + 32 <= p.d_in) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 q = __ldg(reinterpret_cast<const float4*>(x + k + e));
+            v[e] = q.x; v[e + 1] = q.y; v[e + 2] = q.z; v[e + 3] = q.w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = k + e < p.d_in ? x[k + e] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t b[3][4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t lo[3], hi[3];
+            split3(v[8 * j + q], lo);
+            split3(v[8 * j + q + 4], hi);
+#pragma unroll
+            for (int part = 0; part < 3; ++part) b[part][q] = __byte_perm(lo[part], hi[part], 0x7632);
+          }
+#pragma unroll
+          for (int part = 0; part < 3; ++part)
+            xs[((at * 3 + part) * 32 + slot) * 4 + (j ^ ((slot >> 1) & 3))] =
+                make_uint4(b[part][0], b[part][1], b[part][2], b[part][3]);
+        }
+      }
+      __syncthreads();
+      staged += n;
+    }
+    uint32_t xw[STAGED ? 1 : 16];
+    if constexpr (!STAGED) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) xw[i] = 0;
+      if (g < p.batch) load_x(static_cast<const __nv_bfloat16*>(p.X) + g * p.ldx, 128 * (int64_t)step + 32 * t, p.d_in, p.x_vec, xw);
+    }
+    const int n = (step - first) / KW, slot = n & (kDepth - 1);
+    fetch(n + kDepth - 1);   // into the slot that was read in the last step
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    const uint4 w[2] = {code_ring[slot][0][threadIdx.x], code_ring[slot][1][threadIdx.x]};
     uint32_t s[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t r = r0 + g + 8 * h;
-      w[h] = make_uint4(0, 0, 0, 0);
-      s[h] = 0;
-      if (r < p.d_out && k < padded) {
-        w[h] = *reinterpret_cast<const uint4*>(p.codes + r * p.ldc + k / 2);
-        if (FMT == KQ_FP4_MX)
-          s[h] = p.scales[kq::fp4::scale_offset(r, k / 32, p.kat)];
-        else
-          s[h] = *reinterpret_cast<const uint16_t*>(p.scales + kq::fp4::scale_offset(r, k / 16, p.kat));
-      }
+      const uint32_t word = scale_ring[slot][h][threadIdx.x];
+      s[h] = FMT == KQ_FP4_MX ? word >> (8 * t) & 0xffu : word >> (16 * (t & 1)) & 0xffffu;
     }
-    uint32_t b[PARTS][16];
-    load_x<T, PARTS>(x, k, p.d_in, g < p.batch, p.x_vec, b);
+    const bool small = FMT == KQ_FP4_MX && !__any_sync(0xffffffffu, max(s[0], s[1]) > 128u);
     uint32_t sc[2][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      sc[h][0] = scale_pair<FMT>(s[h] & 0xffu);
-      sc[h][1] = FMT == KQ_FP4_MX ? sc[h][0] : scale_pair<FMT>(s[h] >> 8);
+      sc[h][0] = scale_pair<FMT>(s[h] & 0xffu, small);
+      sc[h][1] = FMT == KQ_FP4_MX ? sc[h][0] : scale_pair<FMT>(s[h] >> 8, small);
     }
-    // the tensor core truncates as it accumulates: one chain per 128 columns,
-    // the chains summed in rounded fp32
-    float part_acc[4] = {0.f, 0.f, 0.f, 0.f};
-    const uint32_t w0[4] = {w[0].x, w[0].y, w[0].z, w[0].w}, w1[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
+    // the tensor core truncates as it accumulates: one chain per 128 columns (and
+    // part), the chains summed in rounded fp32, the smallest part first
+    float chain[PARTS][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t s0 = sc[0][j / 2], s1 = sc[1][j / 2];
-      const uint32_t a[8] = {weight<FMT>(spread<0>(w0[j]), s0), weight<FMT>(spread<0>(w1[j]), s1),
-                             weight<FMT>(spread<1>(w0[j]), s0), weight<FMT>(spread<1>(w1[j]), s1),
-                             weight<FMT>(spread<2>(w0[j]), s0), weight<FMT>(spread<2>(w1[j]), s1),
-                             weight<FMT>(spread<3>(w0[j]), s0), weight<FMT>(spread<3>(w1[j]), s1)};
+    for (int c = 0; c < PARTS; ++c)
 #pragma unroll
-      for (int part = 0; part < PARTS; ++part) {
-        mma16816(part_acc, a[0], a[1], a[2], a[3], b[part][4 * j], b[part][4 * j + 1]);
-        mma16816(part_acc, a[4], a[5], a[6], a[7], b[part][4 * j + 2], b[part][4 * j + 3]);
+      for (int i = 0; i < 4; ++i) chain[c][i] = 0.f;
+    const uint4* xstep = xs + (STAGED ? (step - staged + min(kStageSteps, staged - first)) : 0) * PARTS * 128 + lane * 4;
+    auto products = [&](bool sm) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w0 = j == 0 ? w[0].x : (j == 1 ? w[0].y : (j == 2 ? w[0].z : w[0].w));
+        const uint32_t w1 = j == 0 ? w[1].x : (j == 1 ? w[1].y : (j == 2 ? w[1].z : w[1].w));
+        const uint32_t c0 = sc[0][j / 2], c1 = sc[1][j / 2];
+        const uint32_t a[8] = {weight<FMT>(spread<0>(w0), c0, sm), weight<FMT>(spread<0>(w1), c1, sm),
+                               weight<FMT>(spread<1>(w0), c0, sm), weight<FMT>(spread<1>(w1), c1, sm),
+                               weight<FMT>(spread<2>(w0), c0, sm), weight<FMT>(spread<2>(w1), c1, sm),
+                               weight<FMT>(spread<3>(w0), c0, sm), weight<FMT>(spread<3>(w1), c1, sm)};
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) {
+          uint4 b;
+          if constexpr (STAGED)
+            b = xstep[part * 128 + (j ^ ((lane >> 1) & 3))];
+          else
+            b = make_uint4(__byte_perm(xw[4 * j], xw[4 * j + 2], 0x5410), __byte_perm(xw[4 * j], xw[4 * j + 2], 0x7632),
+                           __byte_perm(xw[4 * j + 1], xw[4 * j + 3], 0x5410), __byte_perm(xw[4 * j + 1], xw[4 * j + 3], 0x7632));
+          mma16816(chain[part], a[0], a[1], a[2], a[3], b.x, b.y);
+          mma16816(chain[part], a[4], a[5], a[6], a[7], b.z, b.w);
+        }
       }
+    };
+    if (FMT == KQ_FP4_NV || small)
+      products(true);
+    else
+      products(false);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float sum = chain[PARTS - 1][i];
+#pragma unroll
+      for (int c = PARTS - 2; c >= 0; --c) sum += chain[c][i];
+      acc[i] += sum;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] += part_acc[i];
   }
-  sums[warp][g][2 * t] = acc[0];
-  sums[warp][g][2 * t + 1] = acc[1];
-  sums[warp][g + 8][2 * t] = acc[2];
-  sums[warp][g + 8][2 * t + 1] = acc[3];
-  __syncthreads();
-  if (threadIdx.x < 128) {
-    const int row = threadIdx.x % 16, n = threadIdx.x / 16;
-    const int64_t r = r0 + row;
-    if (n < p.batch && r < p.d_out) {
-      float v = 0.f;
+  float(*mine)[8] = &sums[STAGED ? 0 : warp][STAGED ? 16 * warp : 0];
+  mine[g][2 * t] = acc[0];
+  mine[g][2 * t + 1] = acc[1];
+  mine[g + 8][2 * t] = acc[2];
+  mine[g + 8][2 * t + 1] = acc[3];
+  auto sync = [&] {
+    if (STAGED && p.ks > 1)
+      asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    else
+      __syncthreads();
+  };
+  sync();
+  // the row block's outputs, dealt to the cluster's CTAs
+  const int ctas = STAGED ? p.ks : 1;
+  for (int i = threadIdx.x + kWarps * 32 * rank; i < ROWS * p.batch; i += kWarps * 32 * ctas) {
+    const int row = i % ROWS, n = i / ROWS;
+    const int64_t r = row0 + row;
+    float v[8], y = 0.f;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) v += sums[i][row][n];
-      if (FMT == KQ_FP4_NV) v *= 256.f * (p.g ? *p.g : 1.f);
-      if constexpr (sizeof(T) == 4)
-        static_cast<float*>(p.Y)[n * p.ldy + r] = v;
+    for (int q = 0; q < 8; ++q) {
+      if constexpr (STAGED)
+        v[q] = q < ctas ? (ctas > 1 ? ld_cluster(&sums[0][row][n], q) : sums[0][row][n]) : 0.f;
       else
-        static_cast<__nv_bfloat16*>(p.Y)[n * p.ldy + r] = __float2bfloat16_rn(v);
+        v[q] = sums[q][row][n];
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) y += v[q];
+    if (r < p.d_out) {
+      if (FMT == KQ_FP4_NV) y *= 256.f * (p.g ? *p.g : 1.f);
+      if constexpr (STAGED)
+        static_cast<float*>(p.Y)[n * p.ldy + r] = y;
+      else
+        static_cast<__nv_bfloat16*>(p.Y)[n * p.ldy + r] = __float2bfloat16_rn(y);
     }
   }
+  if (STAGED && p.ks > 1) sync();   // the sums stay until every CTA has read them
 }
 
 template <typename T, int FMT, int ROW_LANES>
@@ -504,9 +630,35 @@ kq_status launch_quantize(const QuantParams& p, cudaStream_t st) {
 }
 
 template <typename T, int FMT>
-kq_status launch_matvec(const MatvecParams& p, cudaStream_t st) {
-  return kq::launch_ex("kq_fp4_matvec", true, matvec_kernel<T, FMT>, dim3((unsigned)kq::cdiv(p.d_out, 16)), dim3(kWarps * 32), 0,
-                       st, p);
+kq_status launch_matvec(MatvecParams p, cudaStream_t st) {
+  const char* what = "kq_fp4_matvec";
+  constexpr bool STAGED = sizeof(T) == 4;
+  const int64_t steps = kq::cdiv(p.d_in, 128);
+  p.ks = !STAGED ? 1 : (steps >= 8 ? 8 : (steps >= 4 ? 4 : (steps >= 2 ? 2 : 1)));
+  const int smem = STAGED ? (int)std::min<int64_t>(kStageSteps, kq::cdiv(steps, p.ks)) * 6144 : 0;
+  // the attribute belongs to the device: set on every call that needs it, as the current device may change
+  if (STAGED)
+    KQ_TRY(kq::cuda_check(cudaFuncSetAttribute(matvec_kernel<T, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kStageSteps * 6144), what));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(kq::cdiv(p.d_out, STAGED ? 16 * kWarps : 16) * p.ks));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.ks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.ks > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, matvec_kernel<T, FMT>, p);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return kq::cuda_check(e, what);
+  }
+  return kq::launch_check(what);
 }
 
 }  // namespace
