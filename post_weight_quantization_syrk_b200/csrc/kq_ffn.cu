@@ -22,11 +22,11 @@ kq_status bf16_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows,
 template <int EPI>
 using GatedPair = Cfg<KIND_BF16, 2, 256, false, false, EPI, 6>;
 template <int EPI>
-using GatedSlim = Cfg<KIND_BF16, 1, 128, false, false, EPI, 4>;
+using GatedSlim = Cfg<KIND_BF16, 1, 128, false, false, EPI, 6>;
 using InputPair = Cfg<KIND_BF16, 2, 256, false, true, EPI_STORE, 6>;
-using InputSlim = Cfg<KIND_BF16, 1, 64, false, true, EPI_STORE, 4>;
+using InputSlim = Cfg<KIND_BF16, 1, 64, false, true, EPI_STORE, 6>;
 using WeightPair = Cfg<KIND_BF16, 2, 256, true, true, EPI_STORE, 6>;
-using WeightSlim = Cfg<KIND_BF16, 1, 128, true, true, EPI_STORE, 4>;
+using WeightSlim = Cfg<KIND_BF16, 1, 128, true, true, EPI_STORE, 6>;
 
 template <class C>
 kq_status go(const char* what, const Maps& m, Params p, int problems, int ks, cudaStream_t st) {

@@ -23,9 +23,9 @@ kq_status scales_map(CUtensorMap* m, const kq_fp4* q, int atoms) {
 template <int KIND, int EPI>
 using Pair = Cfg<KIND, 2, 256, false, false, EPI, 5>;
 template <int KIND, int EPI>
-using Wide = Cfg<KIND, 1, 128, false, false, EPI, 4>;
+using Wide = Cfg<KIND, 1, 128, false, false, EPI, 6>;
 template <int KIND, int EPI>
-using Slim = Cfg<KIND, 1, EPI == EPI_STORE ? 64 : 128, false, false, EPI, 4>;
+using Slim = Cfg<KIND, 1, EPI == EPI_STORE ? 64 : 128, false, false, EPI, 6>;
 
 template <class C>
 kq_status run(const char* what, const kq_fp4* A, const kq_fp4* B0, const kq_fp4* B1, Params p, int ks, cudaStream_t st) {

@@ -11,17 +11,17 @@
 // issuing thread's tcgen05.cp, which runs in turn with the MMAs at about 53
 // cycles a tile (6 tiles, KQ_FP4_MX, or 12, KQ_FP4_NV, beside the 512 MMA cycles
 // of a stage: 0.61 and 0.82 us a stage against 0.43 without them, at 8192 x
-// 11008 x 16384).  CG = 1: the epilogue's four warps, one per lane quarter, with
-// tcgen05.st (the 16 bytes of a tile row are a lane's four columns): it leaves
-// the issue order alone and takes half the columns where an MMA needs half a
-// tile.  Under a dense stream of MMAs these stores wait for TMEM (0.87 us a
-// stage at the size above), so the pair does not use them.
+// 11008 x 16384).  CG = 1: two sets of four warps, taking stages in turn, a warp
+// per lane quarter, with tcgen05.st (the 16 bytes of a tile row are a lane's four
+// columns, of which an MMA of half a tile's rows needs two).  Under the pair's
+// dense stream of MMAs these stores wait for TMEM (0.87 us a stage at the size
+// above); in the 128-row tiles, which stream weights, the copies are what waits.
 //
 // Shapes.  CG = 2: a CTA pair per 256 x 256 tile (cta_group::2), each CTA
 // holding 128 rows of A and of B, so an SM fetches 64 bytes per MMA cycle
-// instead of the 96 of a single 128 x 256 CTA.  CG = 1: 128 x BN tiles for
-// products with few rows, optionally with K split over a cluster of KS CTAs
-// whose fp32 partials are summed in rank order through distributed shared
+// instead of the 96 of a single 128 x 256 CTA.  CG = 1: 128 x BN tiles, one per
+// CTA, for products with few rows, optionally with K split over a cluster of KS
+// CTAs whose fp32 partials are summed in rank order through distributed shared
 // memory (results do not depend on scheduling).
 //
 // Gated tiles hold the gate and the up columns of the same features side by
@@ -40,6 +40,8 @@
 
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "kq_tc.cuh"
 
 namespace kq {
@@ -52,7 +54,7 @@ enum { EPI_STORE = 0, EPI_GATED = 1, EPI_GATED_BWD = 2 };
 
 template <int KIND_, int CG_, int BN_, bool AMN_, bool BMN_, int EPI_, int STAGES_>
 struct Cfg {
-  static constexpr int KIND = KIND_, CG = CG_, BN = BN_, EPI = EPI_, STAGES = STAGES_;
+  static constexpr int KIND = KIND_, CG = CG_, BN = BN_, EPI = EPI_;
   static constexpr bool AMN = AMN_, BMN = BMN_, FP4 = KIND != KIND_BF16, DUAL = EPI != EPI_STORE;
   static constexpr int NSUB = (CG == 1 && DUAL) ? 2 : 1;     // MMAs per K step
   static constexpr int MMA_N = BN / NSUB;
@@ -69,20 +71,26 @@ struct Cfg {
   static constexpr int SFB_W = MMA_N == 64 ? 2 : 4;
   static constexpr int SF_COLS = ATOMS * (4 + SFB_W * SFB_TILES);
   static constexpr int NBUF = (CG == 2 && !FP4) ? 2 : 1;     // accumulators
-  static constexpr int COLS = NBUF * BN + STAGES * SF_COLS;  // a scale buffer per stage
+  // TMEM (two 128-row CTAs to an SM): accumulators, then a scale buffer per stage
+  static constexpr int TMEM_LIMIT = CG == 2 ? 512 : 256;
+  static constexpr int SF_FIT = FP4 ? (TMEM_LIMIT - NBUF * BN) / (FP4 ? SF_COLS : 1) : STAGES_;
+  static constexpr int STAGES = SF_FIT < STAGES_ ? SF_FIT : STAGES_;
+  static constexpr int COLS = NBUF * BN + STAGES * SF_COLS;
   static constexpr int TMEM_COLS = COLS <= 64 ? 64 : (COLS <= 128 ? 128 : (COLS <= 256 ? 256 : 512));
-  static_assert(COLS <= 512, "TMEM");
-  static constexpr int EW = CG == 2 ? 8 : 4;                 // epilogue warps
+  static constexpr int EW = 8;                               // epilogue warps
   static constexpr int EW0 = 2;                              // the first of them
   static constexpr int THREADS = 32 * (EW0 + EW);
   static constexpr int PART_LD = BN + 4;                     // row stride of the split-K partials
-  static constexpr int RING = STAGES * (A_OFF + A_BYTES);
+  static constexpr int RING = STAGES * (A_OFF + A_BYTES);    // at most: stages shrink with A's box, and p.stages may be fewer
   static constexpr int STAGING = EW * 4096;                  // 32 rows x 128 bytes per epilogue warp
-  static constexpr int BARS = 1024;
+  static constexpr int BARS = 1024;                          // barriers, TMEM address, abort flag
   // CG = 1 has one tile per CTA: staging and split-K partials reuse the ring
-  static constexpr int SMEM = 1024 + BARS + RING + (CG == 2 ? STAGING : 0);
+  static constexpr int MIN_STAGES = 4;
+  static constexpr int SMEM = 1024 + BARS + (CG == 2 ? RING + STAGING : MIN_STAGES * (A_OFF + A_BYTES));
   static_assert(SMEM <= 232448, "shared memory");
-  static_assert(CG == 2 || (128 * PART_LD * 4 <= RING && STAGING <= RING), "the ring holds what reuses it");
+  static_assert(CG == 2 || (128 * PART_LD * 4 <= MIN_STAGES * (A_OFF + A_BYTES) && STAGING <= MIN_STAGES * A_OFF),
+                "the ring holds what reuses it");
+  static_assert(STAGES >= MIN_STAGES, "stages");
 };
 
 struct Maps {
@@ -99,6 +107,8 @@ struct Params {
   int a_rows;            // rows of the A box (CG = 1: no more than M needs)
   int kat;               // scale tiles along K per 128 rows
   int ks;                // CTAs sharing a tile along K (CG = 1)
+  int stages;            // of the ring in use
+  int via_smem;          // CG = 1: the accumulators go through shared memory, spread over all threads
   int act;
   int out_f32;
   void* out[2];          // store: Y of each problem; gated: H; backward: dG, dU
@@ -427,23 +437,24 @@ __device__ __forceinline__ uint4 load16(const __nv_bfloat16* row, int64_t c, int
 // piece k ^ (i % 8), so that rows and lines are both free of bank conflicts.
 __device__ __forceinline__ uint32_t piece(uint32_t stg, int i, int k) { return stg + 128 * i + 16 * (k ^ (i & 7)); }
 
-// The staged rows (row 0 = row r0 of the matrix, columns c0..) to global memory,
-// 4 rows of 128 bytes per step; or from it.
-template <typename T>
+// The staged rows (row 0 = row r0 of the matrix, columns c0.., P pieces of 16 bytes
+// each) to global memory, neighbouring lanes taking neighbouring pieces; or from it.
+template <int P, typename T>
 __device__ __forceinline__ void rows_out(uint32_t stg, T* base, int64_t ld, int64_t r0, int64_t M, int64_t c0, int64_t N, int vec) {
-  const int lane = threadIdx.x % 32, k = lane % 8;
+  const int lane = threadIdx.x % 32, k = lane % P;
   __syncwarp();
 #pragma unroll 2
-  for (int i = lane / 8; i < 32; i += 4)
+  for (int i = lane / P; i < 32; i += 32 / P)
     if (r0 + i < M) store16(base + (r0 + i) * ld, c0 + k * (16 / (int)sizeof(T)), N, vec, lds128(piece(stg, i, k)));
   __syncwarp();
 }
+template <int P>
 __device__ __forceinline__ void rows_in(uint32_t stg, const __nv_bfloat16* base, int64_t ld, int64_t r0, int64_t M, int64_t c0,
                                         int64_t N, int vec) {
-  const int lane = threadIdx.x % 32, k = lane % 8;
+  const int lane = threadIdx.x % 32, k = lane % P;
   __syncwarp();
 #pragma unroll 2
-  for (int i = lane / 8; i < 32; i += 4)
+  for (int i = lane / P; i < 32; i += 32 / P)
     sts128(piece(stg, i, k), r0 + i < M ? load16(base + (r0 + i) * ld, c0 + 8 * k, N, vec) : make_uint4(0, 0, 0, 0));
   __syncwarp();
 }
@@ -587,24 +598,19 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
   pdl_trigger();
   const uint32_t sf0 = tmem + C::NBUF * C::BN;
 
-  // The scales of stages kb0 .. kb1 of a tile, by one of the four warps that write them.
-  int sc_stage = 0;
-  uint32_t sc_phase = 0;
-  auto write_scales = [&](int tn) {
-    for (int kb = kb0; kb < kb1; ++kb) {
-      if (!warp_wait(landed0 + 8 * sc_stage, sc_phase, abort_flag, p.info, 14, p.wait_ns)) return false;
+  // CG = 1: the scales of this CTA's stages, every second one, by one warp of a set.
+  auto write_scales = [&](int set, int tn) {
+    for (int i = set; i < kb1 - kb0; i += 2) {
+      const uint32_t stage = (uint32_t)i % p.stages;
+      if (!warp_wait(landed0 + 8 * stage, ((uint32_t)i / p.stages) & 1u, abort_flag, p.info, 14, p.wait_ns)) return false;
       // the slot's last MMAs are done: the producer waited for them before this stage's copies
       fence_after();
       if constexpr (C::FP4)
-        scales_to_tmem<C>(ring + sc_stage * stage_bytes + C::B_BYTES,
-                          sf0 + sc_stage * C::SF_COLS + ((uint32_t)(32 * (warp & 3)) << 16), tn & 1);
+        scales_to_tmem<C>(ring + stage * stage_bytes + C::B_BYTES,
+                          sf0 + stage * C::SF_COLS + ((uint32_t)(32 * (warp & 3)) << 16), tn & 1);
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ready0 + 8 * sc_stage);
-      if (++sc_stage == S) {
-        sc_stage = 0;
-        sc_phase ^= 1u;
-      }
+      if (lane == 0) mbar_arrive(ready0 + 8 * stage);
     }
     return true;
   };
@@ -663,7 +669,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
         }
         issued |= 1u << stage;
         issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-        if (++stage == S) {
+        if (++stage == p.stages) {
           stage = 0;
           phase ^= 1u;
         }
@@ -742,7 +748,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
           }
           any = true;
           commit<CG>(on, empty0 + 8 * stage);   // the stage is free once these MMAs have read it
-          if (++stage == S) {
+          if (++stage == p.stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -755,7 +761,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
         }
       }
       if (any) {
-        // every MMA this thread issued has completed before TMEM is released
+        // every MMA and copy this thread issued has completed before TMEM is released
         commit_local<CG>(on, drained);
         if (on) mbar_drain(drained, 0);
       }
@@ -764,8 +770,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
     // ---------------- epilogue: lane quarter warp % 4, one row per lane
     const int wq = warp & 3, share = (warp - C::EW0) / 4;
     constexpr int CW = C::OUTC / (C::EW / 4);   // output columns of this warp
-    constexpr int CH = CW < 64 ? CW : 64;       // taken 64 at a time
-    static_assert(CH == 64, "64 output columns at a time");
+    constexpr int CH = CW < 64 ? CW : 64;       // taken 64 or 32 at a time
+    static_assert(CH == 64 || CH == 32, "64 or 32 output columns at a time");
     const uint32_t stg = (CG == 2 ? ring + C::RING : ring) + 4096 * (warp - C::EW0);
     const float sa = (p.ga ? *p.ga : 1.f) * (p.gb[0] ? *p.gb[0] : 1.f);
     const float su = (p.ga ? *p.ga : 1.f) * (p.gb[1] ? *p.gb[1] : 1.f);
@@ -776,7 +782,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
       int tm, tn;
       tile_coords(p, t - problem * p.problem_tiles, &tm, &tn);
       if constexpr (C::FP4 && CG == 1) {
-        if (!write_scales(tn)) break;
+        if (!write_scales(share, tn)) break;
       }
       const int64_t r0 = (int64_t)tm * 128 * CG + rank * 128 + 32 * wq;   // lane 0's row
       const int64_t c0 = (int64_t)tn * C::OUTC + share * CW;
@@ -793,14 +799,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
             mbar_arrive(accempty0 + 8 * buf);
         }
       };
-      if (ks > 1) {
-        // fp32 partials to this CTA's shared memory, summed below
+      if (CG == 1 && p.via_smem) {
+        // fp32 sums (or partial sums) to this CTA's shared memory, finished below
         float* part = reinterpret_cast<float*>(smem + C::BARS);
         if (r0 < p.M) {
 #pragma unroll 1
-          for (int c = 0; c < C::BN; c += 16) {
+          for (int c = share * (C::BN / 2); c < (share + 1) * (C::BN / 2); c += 16) {
             float v[16];
-            tmem_ld16(d + c, v);
+            tmem_ld16(tmem + ((uint32_t)(32 * wq) << 16) + c, v);
             if (r0 + lane < p.M) {
 #pragma unroll
               for (int i = 0; i < 16; i += 4)
@@ -811,75 +817,74 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
         }
         release();
       } else if constexpr (C::EPI == EPI_STORE) {
-        auto put = [&](int c, float* v) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i) v[i] *= sa;
-          if (p.out_f32) {
-#pragma unroll
-            for (int h = 0; h < 64; h += 32) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const uint32_t* w = reinterpret_cast<const uint32_t*>(v + h + 4 * k);
-                sts128(piece(stg, lane, k), make_uint4(w[0], w[1], w[2], w[3]));
-              }
-              rows_out(stg, static_cast<float*>(p.out[problem]), p.ldo[problem], r0, p.M, c0 + c + h, p.N, p.out_vec[problem]);
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sts128(piece(stg, lane, k), pack8(v + 8 * k));
-            rows_out(stg, static_cast<__nv_bfloat16*>(p.out[problem]), p.ldo[problem], r0, p.M, c0 + c, p.N,
-                     p.out_vec[problem]);
-          }
-        };
         if (DRAIN && !p.out_f32) {
           uint4 q[CW / 8];
 #pragma unroll
-          for (int c = 0; c < CW; c += 64) {
-            float v[64];
+          for (int c = 0; c < CW; c += 32) {
+            float v[32];
             tmem_ld32(d + c, v);
-            tmem_ld32(d + c + 32, v + 32);
 #pragma unroll
-            for (int i = 0; i < 64; ++i) v[i] *= sa;
+            for (int i = 0; i < 32; ++i) v[i] *= sa;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) q[c / 8 + k] = pack8(v + 8 * k);
+            for (int k = 0; k < 4; ++k) q[c / 8 + k] = pack8(v + 8 * k);
           }
           release();
 #pragma unroll
-          for (int c = 0; c < CW; c += 64) {
+          for (int c = 0; c < CW; c += CH) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sts128(piece(stg, lane, k), q[c / 8 + k]);
-            rows_out(stg, static_cast<__nv_bfloat16*>(p.out[problem]), p.ldo[problem], r0, p.M, c0 + c, p.N,
-                     p.out_vec[problem]);
+            for (int k = 0; k < CH / 8; ++k) sts128(piece(stg, lane, k), q[c / 8 + k]);
+            rows_out<CH / 8>(stg, static_cast<__nv_bfloat16*>(p.out[problem]), p.ldo[problem], r0, p.M, c0 + c, p.N,
+                             p.out_vec[problem]);
           }
         } else {
 #pragma unroll 1
-          for (int c = 0; c < CW; c += 64) {
-            float v[64];
-            tmem_ld32(d + c, v);
-            tmem_ld32(d + c + 32, v + 32);
-            if (c + 64 == CW) release();
-            put(c, v);
+          for (int c = 0; c < CW; c += CH) {
+            float v[CH];
+#pragma unroll
+            for (int h = 0; h < CH; h += 32) tmem_ld32(d + c + h, v + h);
+            if (c + CH == CW) release();
+#pragma unroll
+            for (int i = 0; i < CH; ++i) v[i] *= sa;
+            if (p.out_f32) {
+#pragma unroll
+              for (int h = 0; h < CH; h += 32) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const uint32_t* w = reinterpret_cast<const uint32_t*>(v + h + 4 * k);
+                  sts128(piece(stg, lane, k), make_uint4(w[0], w[1], w[2], w[3]));
+                }
+                rows_out<8>(stg, static_cast<float*>(p.out[problem]), p.ldo[problem], r0, p.M, c0 + c + h, p.N,
+                            p.out_vec[problem]);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < CH / 8; ++k) sts128(piece(stg, lane, k), pack8(v + 8 * k));
+              rows_out<CH / 8>(stg, static_cast<__nv_bfloat16*>(p.out[problem]), p.ldo[problem], r0, p.M, c0 + c, p.N,
+                               p.out_vec[problem]);
+            }
           }
         }
       } else if constexpr (C::EPI == EPI_GATED) {
-        float g[64], u[64];
-        tmem_ld32(d, g);
-        tmem_ld32(d + 32, g + 32);
-        tmem_ld32(d + C::BN / 2, u);
-        tmem_ld32(d + C::BN / 2 + 32, u + 32);
+        static_assert(CW == CH, "one piece per warp");
+        float g[CH], u[CH];
+#pragma unroll
+        for (int h = 0; h < CH; h += 32) tmem_ld32(d + h, g + h);
+#pragma unroll
+        for (int h = 0; h < CH; h += 32) tmem_ld32(d + C::BN / 2 + h, u + h);
         release();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < CH / 8; ++k) {
 #pragma unroll
           for (int i = 8 * k; i < 8 * k + 8; ++i) g[i] = (sa * g[i]) * gate_of(sa * g[i], p.act).p * (su * u[i]);
           sts128(piece(stg, lane, k), pack8(g + 8 * k));
         }
-        rows_out(stg, static_cast<__nv_bfloat16*>(p.out[0]), p.ldo[0], r0, p.M, c0, p.N, p.out_vec[0]);
+        rows_out<CH / 8>(stg, static_cast<__nv_bfloat16*>(p.out[0]), p.ldo[0], r0, p.M, c0, p.N, p.out_vec[0]);
       } else {
-        rows_in(stg, p.dh, p.lddh, r0, p.M, c0, p.N, p.dh_vec);
-        uint4 og[8], ou[8], oh[8];
+        static_assert(CW == CH, "one piece per warp");
+        rows_in<CH / 8>(stg, p.dh, p.lddh, r0, p.M, c0, p.N, p.dh_vec);
+        uint4 og[CH / 8], ou[CH / 8], oh[CH / 8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < CH / 32; ++h) {
           float g[32], u[32];
           tmem_ld32(d + 32 * h, g);
           tmem_ld32(d + C::BN / 2 + 32 * h, u);
@@ -902,15 +907,15 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
         release();
         __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sts128(piece(stg, lane, k), og[k]);
-        rows_out(stg, static_cast<__nv_bfloat16*>(p.out[0]), p.ldo[0], r0, p.M, c0, p.N, p.out_vec[0]);
+        for (int k = 0; k < CH / 8; ++k) sts128(piece(stg, lane, k), og[k]);
+        rows_out<CH / 8>(stg, static_cast<__nv_bfloat16*>(p.out[0]), p.ldo[0], r0, p.M, c0, p.N, p.out_vec[0]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sts128(piece(stg, lane, k), ou[k]);
-        rows_out(stg, static_cast<__nv_bfloat16*>(p.out[1]), p.ldo[1], r0, p.M, c0, p.N, p.out_vec[1]);
+        for (int k = 0; k < CH / 8; ++k) sts128(piece(stg, lane, k), ou[k]);
+        rows_out<CH / 8>(stg, static_cast<__nv_bfloat16*>(p.out[1]), p.ldo[1], r0, p.M, c0, p.N, p.out_vec[1]);
         if (p.h) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) sts128(piece(stg, lane, k), oh[k]);
-          rows_out(stg, p.h, p.ldh, r0, p.M, c0, p.N, p.h_vec);
+          for (int k = 0; k < CH / 8; ++k) sts128(piece(stg, lane, k), oh[k]);
+          rows_out<CH / 8>(stg, p.h, p.ldh, r0, p.M, c0, p.N, p.h_vec);
         }
       }
       if (++buf == C::NBUF) {
@@ -923,9 +928,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
   fence_before();
   __syncthreads();
   if constexpr (CG == 1) {
-    if (ks > 1) {
+    if (p.via_smem) {
       // sum of the cluster's partials in rank order; each CTA takes a share of the tile's columns
-      cluster_sync();
+      if (ks > 1) cluster_sync();
       const int problem = unit0 / p.problem_tiles;
       int tm, tn;
       tile_coords(p, unit0 - problem * p.problem_tiles, &tm, &tn);
@@ -939,34 +944,37 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
         float a[8], u[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) a[e] = u[e] = 0.f;
-        // the loads of all CTAs' pieces are in flight together
-        float4 x[8][C::DUAL ? 4 : 2];
+        // the loads of four CTAs' pieces are in flight together
+#pragma unroll 1
+        for (int q0 = 0; q0 < ks; q0 += 4) {
+          float4 x[4][C::DUAL ? 4 : 2];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          if (q < ks) {
-            const uint32_t src = mapa(at, (uint32_t)q);
-            x[q][0] = ld_cluster(src);
-            x[q][1] = ld_cluster(src + 16);
-            if constexpr (C::DUAL) {
-              x[q][2] = ld_cluster(src + 2 * C::BN);
-              x[q][3] = ld_cluster(src + 2 * C::BN + 16);
+          for (int q = 0; q < 4; ++q) {
+            if (q0 + q < ks) {
+              const uint32_t src = ks > 1 ? mapa(at, (uint32_t)(q0 + q)) : at;
+              x[q][0] = ld_cluster(src);
+              x[q][1] = ld_cluster(src + 16);
+              if constexpr (C::DUAL) {
+                x[q][2] = ld_cluster(src + 2 * C::BN);
+                x[q][3] = ld_cluster(src + 2 * C::BN + 16);
+              }
             }
           }
-        }
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          if (q < ks) {
-            const float* f = reinterpret_cast<const float*>(x[q]);
+          for (int q = 0; q < 4; ++q) {
+            if (q0 + q < ks) {
+              const float* f = reinterpret_cast<const float*>(x[q]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              a[e] += f[e];
-              if constexpr (C::DUAL) u[e] += f[8 + e];
+              for (int e = 0; e < 8; ++e) {
+                a[e] += f[e];
+                if constexpr (C::DUAL) u[e] += f[8 + e];
+              }
             }
           }
         }
         finish8<C::EPI>(p, problem, (int64_t)tm * 128 + rr, (int64_t)tn * C::OUTC + c, sa, su, a, u);
       }
-      cluster_sync();                              // the partials stay until every CTA has read them
+      if (ks > 1) cluster_sync();                  // the partials stay until every CTA has read them
     }
   } else {
     cluster_sync();                                // both CTAs are done with each other's memory
@@ -979,12 +987,24 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
 
 // ------------------------------------------------------------------ host
 
+// Bytes of shared memory with `stages` of A boxes of a_rows rows: the last stage's
+// MMAs still read 128 rows from its A on.
 template <class C>
-kq_status launch(const char* what, const Maps& maps, const Params& p, int grid, cudaStream_t st) {
-  // shorter A boxes make shorter stages; the last stage's MMAs still read 128 rows from its A on
-  const int smem = C::SMEM - (C::STAGES - 1) * (128 - p.a_rows) * 128;
+constexpr int smem_of(int stages, int a_rows) {
+  return 1024 + C::BARS + stages * (C::A_OFF + 128 * a_rows) + (128 - a_rows) * 128 + (C::CG == 2 ? C::STAGING : 0);
+}
+
+template <class C>
+kq_status launch(const char* what, const Maps& maps, Params p, int grid, cudaStream_t st) {
+  // CG = 1: as many stages as leave room for two CTAs to an SM (113 KB each), at least MIN_STAGES
+  p.stages = C::STAGES;
+  while (C::CG == 1 && p.stages > C::MIN_STAGES && smem_of<C>(p.stages, p.a_rows) > 113 * 1024) --p.stages;
+  const int smem = smem_of<C>(p.stages, p.a_rows);
+  // few rows: one of the four lane quarters holds them all, so the other warps help through shared memory
+  p.via_smem = C::CG == 1 && (p.ks > 1 || p.M <= 32);
   // the attribute belongs to the device: set on every call, as the current device may change
-  KQ_TRY(cuda_check(cudaFuncSetAttribute(tile_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM), what));
+  KQ_TRY(cuda_check(cudaFuncSetAttribute(tile_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         std::max(C::SMEM, 113 * 1024)), what));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(C::THREADS);
