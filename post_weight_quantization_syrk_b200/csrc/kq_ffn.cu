@@ -24,7 +24,7 @@ using GatedPair = Cfg<KIND_BF16, 2, 256, false, false, EPI, 6>;
 template <int EPI>
 using GatedSlim = Cfg<KIND_BF16, 1, 128, false, false, EPI, 6>;
 using InputPair = Cfg<KIND_BF16, 2, 256, false, true, EPI_STORE, 6>;
-using InputSlim = Cfg<KIND_BF16, 1, 64, false, true, EPI_STORE, 6>;
+using InputSlim = Cfg<KIND_BF16, 1, 128, false, true, EPI_STORE, 6>;
 using WeightPair = Cfg<KIND_BF16, 2, 256, true, true, EPI_STORE, 6>;
 using WeightSlim = Cfg<KIND_BF16, 1, 128, true, true, EPI_STORE, 6>;
 
@@ -34,23 +34,11 @@ kq_status go(const char* what, const Maps& m, Params p, int problems, int ks, cu
   p.tiles_n = (int)kq::cdiv(p.N, C::OUTC);
   p.problem_tiles = p.tiles_m * p.tiles_n;
   p.num_tiles = problems * p.problem_tiles;
-  p.ks = std::min(ks, p.kblocks);
-  while (p.ks & (p.ks - 1)) --p.ks;   // 1, 2, 4 or 8
-  int grid = p.num_tiles * C::CG * p.ks;
-  if (C::CG == 2) {
-    int dev = 0, sms = 0;
-    KQ_TRY(kq::cuda_check(cudaGetDevice(&dev), what));
-    KQ_TRY(kq::cuda_check(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), what));
-    grid = std::min(grid, sms / 2 * 2);
-  }
-  return launch<C>(what, m, p, grid, st);
+  p.ks = ks;
+  return launch<C>(what, m, p, st);
 }
 
-int split_of(int64_t tiles) {
-  int ks = 1;
-  while (ks < 8 && tiles * ks * 2 <= 296) ks *= 2;
-  return ks;
-}
+constexpr Cost kGated = {0.46, 0.38}, kStore = {0.36, 0.33};
 
 struct Shape {
   int64_t T, d, f;
@@ -63,7 +51,8 @@ kq_status gated(const char* what, const Shape& s, const uint16_t* X, int64_t ldx
   p.M = s.T;
   p.N = s.f;
   p.kblocks = p.seg_blocks = (int)kq::cdiv(s.d, 64);
-  const bool pair = s.T > 128 && kq::cdiv(s.T, 256) * kq::cdiv(s.f, 128) >= 48;
+  const Plan plan = make_plan(s.T, kq::cdiv(s.T, 128) * kq::cdiv(s.f, 64), kq::cdiv(s.T, 256) * kq::cdiv(s.f, 128), p.kblocks, kGated);
+  const bool pair = plan.pair;
   p.a_rows = pair ? 128 : (int)std::min<int64_t>(128, kq::cdiv(s.T, 8) * 8);
   Maps m;
   KQ_TRY(bf16_map(&m.a[0], X, s.d, s.T, ldx, p.a_rows));
@@ -71,7 +60,7 @@ kq_status gated(const char* what, const Shape& s, const uint16_t* X, int64_t ldx
   KQ_TRY(bf16_map(&m.b[1], Wu, s.d, s.f, ldw, pair ? 128 : 64));
   m.a[1] = m.sfa = m.sfb[0] = m.sfb[1] = m.a[0];
   if (pair) return go<GatedPair<EPI>>(what, m, p, 1, 1, st);
-  return go<GatedSlim<EPI>>(what, m, p, 1, split_of(kq::cdiv(s.T, 128) * kq::cdiv(s.f, 64)), st);
+  return go<GatedSlim<EPI>>(what, m, p, 1, plan.ks, st);
 }
 
 kq_status check(const char* what, const Shape& s, const uint16_t* X, int64_t ldx, const uint16_t* Wg, const uint16_t* Wu,
@@ -170,7 +159,8 @@ extern "C" kq_status kq_gated_ffn_backward(const uint16_t* X, int64_t tokens, in
     p.out_vec[0] = kq::aligned(dX, 16) && lddx % 8 == 0;
     p.info = info;
     p.wait_ns = kq::wait_limit_ns();
-    const bool pair = tokens > 128 && kq::cdiv(tokens, 256) * kq::cdiv(d, 256) >= 48;
+    const Plan plan = make_plan(tokens, kq::cdiv(tokens, 128) * kq::cdiv(d, 128), kq::cdiv(tokens, 256) * kq::cdiv(d, 256), p.kblocks, kStore);
+    const bool pair = plan.pair;
     p.a_rows = pair ? 128 : (int)std::min<int64_t>(128, kq::cdiv(tokens, 8) * 8);
     Maps m;
     KQ_TRY(bf16_map(&m.a[0], dG, f, tokens, ldg, p.a_rows));
@@ -181,7 +171,7 @@ extern "C" kq_status kq_gated_ffn_backward(const uint16_t* X, int64_t tokens, in
     if (pair)
       KQ_TRY(go<InputPair>(what, m, p, 1, 1, st));
     else
-      KQ_TRY(go<InputSlim>(what, m, p, 1, split_of(kq::cdiv(tokens, 128) * kq::cdiv(d, 64)), st));
+      KQ_TRY(go<InputSlim>(what, m, p, 1, plan.ks, st));
   }
   if (dW_gate) {
     // dWg [f, d] = dG^T X and dWu = dU^T X: two problems of one grid, K = tokens
@@ -202,10 +192,11 @@ extern "C" kq_status kq_gated_ffn_backward(const uint16_t* X, int64_t tokens, in
     KQ_TRY(bf16_map(&m.a[1], dU, f, tokens, ldg, 64));
     KQ_TRY(bf16_map(&m.b[0], X, d, tokens, ldx, 64));
     m.b[1] = m.sfa = m.sfb[0] = m.sfb[1] = m.b[0];
-    if (2 * kq::cdiv(f, 256) * kq::cdiv(d, 256) >= 48)
+    const Plan plan = make_plan(std::max<int64_t>(f, 65), 2 * kq::cdiv(f, 128) * kq::cdiv(d, 128), 2 * kq::cdiv(f, 256) * kq::cdiv(d, 256), p.kblocks, kStore);
+    if (plan.pair)
       KQ_TRY(go<WeightPair>(what, m, p, 2, 1, st));
     else
-      KQ_TRY(go<WeightSlim>(what, m, p, 2, 1, st));
+      KQ_TRY(go<WeightSlim>(what, m, p, 2, plan.ks, st));
   }
   kq::clear_error();
   return KQ_OK;

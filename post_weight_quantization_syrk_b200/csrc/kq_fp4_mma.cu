@@ -23,9 +23,7 @@ kq_status scales_map(CUtensorMap* m, const kq_fp4* q, int atoms) {
 template <int KIND, int EPI>
 using Pair = Cfg<KIND, 2, 256, false, false, EPI, 5>;
 template <int KIND, int EPI>
-using Wide = Cfg<KIND, 1, 128, false, false, EPI, 6>;
-template <int KIND, int EPI>
-using Slim = Cfg<KIND, 1, EPI == EPI_STORE ? 64 : 128, false, false, EPI, 6>;
+using Slim = Cfg<KIND, 1, 128, false, false, EPI, 6>;   // 128 columns, or 64 features
 
 template <class C>
 kq_status run(const char* what, const kq_fp4* A, const kq_fp4* B0, const kq_fp4* B1, Params p, int ks, cudaStream_t st) {
@@ -49,29 +47,18 @@ kq_status run(const char* what, const kq_fp4* A, const kq_fp4* B0, const kq_fp4*
   p.steps = (int)kq::cdiv(A->cols, 64);
   p.kblocks = p.seg_blocks = (int)kq::cdiv(A->cols, 256);
   p.kat = (int)kq::fp4::scale_tiles(A->cols, A->format);
-  p.ks = std::min(ks, p.kblocks);
-  while (p.ks & (p.ks - 1)) --p.ks;   // 1, 2, 4 or 8
-  int grid = p.num_tiles * C::CG * p.ks;
-  if (C::CG == 2) {
-    int dev = 0, sms = 0;
-    KQ_TRY(kq::cuda_check(cudaGetDevice(&dev), what));
-    KQ_TRY(kq::cuda_check(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), what));
-    grid = std::min(grid, sms / 2 * 2);
-  }
-  return launch<C>(what, m, p, grid, st);
+  p.ks = ks;
+  return launch<C>(what, m, p, st);
 }
 
 template <int KIND, int EPI>
 kq_status choose(const char* what, const kq_fp4* A, const kq_fp4* B0, const kq_fp4* B1, const Params& p, cudaStream_t st) {
-  const int64_t outc = EPI == EPI_STORE ? 256 : 128;
-  const int64_t pairs = kq::cdiv(p.M, 256) * kq::cdiv(p.N, outc);
-  if (p.M > 128 && pairs >= 48) return run<Pair<KIND, EPI>>(what, A, B0, B1, p, 1, st);
-  if (p.M > 128) return run<Wide<KIND, EPI>>(what, A, B0, B1, p, 1, st);
-  // few rows: K split until about 256 CTAs stream the weights
-  const int64_t tiles = kq::cdiv(p.N, 64);
-  int ks = 1;
-  while (ks < 8 && tiles * ks * 2 <= 296) ks *= 2;
-  return run<Slim<KIND, EPI>>(what, A, B0, B1, p, ks, st);
+  constexpr bool MX = KIND == KIND_MX;
+  constexpr Cost cost = EPI == EPI_STORE ? Cost{0.6, MX ? 0.62 : 0.82} : Cost{0.7, MX ? 0.64 : 0.85};
+  const Plan plan = make_plan(p.M, kq::cdiv(p.M, 128) * kq::cdiv(p.N, Slim<KIND, EPI>::OUTC),
+                              kq::cdiv(p.M, 256) * kq::cdiv(p.N, Pair<KIND, EPI>::OUTC), kq::cdiv(A->cols, 256), cost);
+  if (plan.pair) return run<Pair<KIND, EPI>>(what, A, B0, B1, p, 1, st);
+  return run<Slim<KIND, EPI>>(what, A, B0, B1, p, plan.ks, st);
 }
 
 }  // namespace

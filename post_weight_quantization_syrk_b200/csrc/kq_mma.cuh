@@ -987,6 +987,56 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
 
 // ------------------------------------------------------------------ host
 
+// Which tiles a product runs on: CTA pairs, or 128-row tiles with K over ks CTAs.
+struct Plan {
+  bool pair;
+  int ks;
+};
+
+// Microseconds a wave of tiles takes per stage of K, measured (B200, 1.9 GHz): 128-row
+// tiles and pairs.  Beside them a wave of 128-row tiles costs about 3 us and one of
+// pairs 2, a launch of pairs 4, and a split of K 2.5 + ks / 2.
+struct Cost {
+  double slim, pair;
+};
+
+// M rows, `slim` and `pairs` tiles of either kind, `stages` of K.  Up to 64 rows the
+// product streams its weights: K is split until the CTAs, two to an SM, are about as
+// many as the SMs (11008 x 4096, 16 rows, MX: 9.9 us with 172 CTAs, 11.4 with 86, 15.4
+// with 344).  Above, the cheaper by the sums above (1024 x 4096 x 4096: 15.7 us on 64
+// pairs, 22.4 on 256 tiles; 512 rows: 14.8 on 32 pairs, 11.5 on 128 tiles; 333 x 1001 x
+// 5460: 16.4 us with K over 4 CTAs, 30.0 without).
+inline Plan make_plan(int64_t M, int64_t slim, int64_t pairs, int64_t stages, Cost c) {
+  constexpr int64_t kSms = 148, kPairs = 74;
+  if (M <= 64) {
+    int ks = 1;
+    while (ks < 8 && slim * ks * 2 <= 176 && ks * 2 <= stages) ks *= 2;
+    return {false, ks};
+  }
+  Plan best = {true, 1};
+  double t = 4 + (2 + c.pair * (double)stages) * (double)cdiv(pairs, kPairs);
+  for (int ks = 1; ks <= 8 && ks <= stages && (ks == 1 || slim * ks <= kSms); ks *= 2) {
+    const double u = (3 + c.slim * (double)cdiv(stages, ks)) * (double)cdiv(slim * ks, kSms) + (ks > 1 ? 2.5 + 0.5 * ks : 0);
+    if (u < t) {
+      t = u;
+      best = {false, ks};
+    }
+  }
+  return best;
+}
+
+// Number of CTAs: a pair's tiles are walked by as many pairs as the GPU holds.
+template <class C>
+kq_status grid_of(const char* what, const Params& p, int* grid) {
+  *grid = p.num_tiles * C::CG * p.ks;
+  if (C::CG == 1) return KQ_OK;
+  int dev = 0, sms = 0;
+  KQ_TRY(cuda_check(cudaGetDevice(&dev), what));
+  KQ_TRY(cuda_check(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), what));
+  *grid = std::min(*grid, sms / 2 * 2);
+  return KQ_OK;
+}
+
 // Bytes of shared memory with `stages` of A boxes of a_rows rows: the last stage's
 // MMAs still read 128 rows from its A on.
 template <class C>
@@ -995,7 +1045,9 @@ constexpr int smem_of(int stages, int a_rows) {
 }
 
 template <class C>
-kq_status launch(const char* what, const Maps& maps, Params p, int grid, cudaStream_t st) {
+kq_status launch(const char* what, const Maps& maps, Params p, cudaStream_t st) {
+  int grid;
+  KQ_TRY(grid_of<C>(what, p, &grid));
   // CG = 1: as many stages as leave room for two CTAs to an SM (113 KB each), at least MIN_STAGES
   p.stages = C::STAGES;
   while (C::CG == 1 && p.stages > C::MIN_STAGES && smem_of<C>(p.stages, p.a_rows) > 113 * 1024) --p.stages;
