@@ -7,15 +7,17 @@
 // E4M3 scale per 16).  In all of them a pipeline stage holds 128 bytes of K
 // per row (64 bf16 or 256 codes, four MMA steps of 32 bytes) in the 128-byte
 // swizzle.  Scale bytes travel as whole 512-byte tiles (128 rows x 4 blocks) by
-// TMA to shared memory and from there to TMEM in one of two ways.  CG = 2: the
-// issuing thread's tcgen05.cp, which runs in turn with the MMAs at about 53
-// cycles a tile (6 tiles, KQ_FP4_MX, or 12, KQ_FP4_NV, beside the 512 MMA cycles
-// of a stage: 0.61 and 0.82 us a stage against 0.43 without them, at 8192 x
-// 11008 x 16384).  CG = 1: two sets of four warps, taking stages in turn, a warp
-// per lane quarter, with tcgen05.st (the 16 bytes of a tile row are a lane's four
-// columns, of which an MMA of half a tile's rows needs two).  Under the pair's
-// dense stream of MMAs these stores wait for TMEM (0.87 us a stage at the size
-// above); in the 128-row tiles, which stream weights, the copies are what waits.
+// TMA to shared memory and from there to TMEM in one of two ways.  CG = 2: by
+// tcgen05.cp, issued by a warp of its own ahead of the MMAs.  (From the thread that
+// issues the MMAs the copies run in turn with them, about 53 cycles a tile, 6 tiles
+// with KQ_FP4_MX or 12 with KQ_FP4_NV beside the 512 MMA cycles of a stage: 0.60
+// and 0.83 us a stage, against 0.47 and 0.57 from another warp, at 8192 x 11008 x
+// 16384.)  CG = 1: two sets of four warps, taking stages in turn, a warp per lane
+// quarter, with tcgen05.st (the 16 bytes of a tile row are a lane's four columns,
+// of which an MMA of half a tile's rows needs two, so that TMEM holds a buffer per
+// stage for two CTAs).  Under the pair's dense stream of MMAs these stores wait for
+// TMEM (0.87 us a stage); in the 128-row tiles they beat the copies (16 x 4096 x
+// 11008 gated, NV: 20.4 us against 26.0).
 //
 // Shapes.  CG = 2: a CTA pair per 256 x 256 tile (cta_group::2), each CTA
 // holding 128 rows of A and of B, so an SM fetches 64 bytes per MMA cycle
@@ -29,11 +31,11 @@
 // second the up rows; with CG = 1 two MMAs per step.  The epilogue then has
 // both projections of a feature in one thread.
 //
-// Warp roles: 0 TMA, 1 TMEM and MMA issue, the others the epilogue (one lane per
-// row, output through a swizzled staging buffer so that rows leave in full
-// 128-byte lines).  With CG = 2 bf16 has two accumulators used in turn; beside
-// the scales only one fits, which the epilogue takes into registers whole, so
-// that the next tile's MMAs wait for that read only.
+// Warp roles: 0 TMA, 1 TMEM and MMA issue, 2-9 the epilogue (one lane per row, two
+// warps per lane quarter, output through a swizzled staging buffer so that rows
+// leave in full lines), 10 the scale copies of a pair.  With CG = 2 bf16 has two
+// accumulators used in turn; beside the scales only one fits, which the epilogue
+// takes into registers whole, so that the next tile's MMAs wait for that read only.
 // Every mbarrier wait is bounded by a time limit; on expiry the kernel
 // records KQ_ERR_TIMEOUT, drains its copies (bounded), frees TMEM and returns.
 #pragma once
@@ -79,7 +81,8 @@ struct Cfg {
   static constexpr int TMEM_COLS = COLS <= 64 ? 64 : (COLS <= 128 ? 128 : (COLS <= 256 ? 256 : 512));
   static constexpr int EW = 8;                               // epilogue warps
   static constexpr int EW0 = 2;                              // the first of them
-  static constexpr int THREADS = 32 * (EW0 + EW);
+  static constexpr int SCALE_WARP = EW0 + EW;                // of a pair
+  static constexpr int THREADS = 32 * (EW0 + EW + (FP4 && CG == 2 ? 1 : 0));
   static constexpr int PART_LD = BN + 4;                     // row stride of the split-K partials
   static constexpr int RING = STAGES * (A_OFF + A_BYTES);    // at most: stages shrink with A's box, and p.stages may be fewer
   static constexpr int STAGING = EW * 4096;                  // 32 rows x 128 bytes per epilogue warp
@@ -556,8 +559,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
   // bars: full [0, S), empty [S, 2S), scales landed [2S, 3S), scales in TMEM
-  // [3S, 4S), acc full [4S, 4S + 2), acc empty [4S + 2, 4S + 4), drained [4S + 4]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * S + 5);
+  // [3S, 4S), acc full [4S, 4S + 2), acc empty [4S + 2, 4S + 4), MMAs drained
+  // [4S + 4], scale copies drained [4S + 5]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * S + 6);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S, landed0 = full0 + 16 * S, ready0 = full0 + 24 * S;
   const uint32_t accfull0 = full0 + 32 * S, accempty0 = accfull0 + 16, drained = accfull0 + 32;
@@ -577,13 +581,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
       mbar_init(landed0 + 8 * s, 1);
-      mbar_init(ready0 + 8 * s, 4);
+      mbar_init(ready0 + 8 * s, CG == 2 ? 1 : 4);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accfull0 + 8 * b, 1);
       mbar_init(accempty0 + 8 * b, CG * C::EW);
     }
     mbar_init(drained, 1);
+    mbar_init(drained + 8, 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
@@ -699,23 +704,12 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
         const uint32_t d = tmem + buf * C::BN;
         for (int kb = kb0; kb < kb1; ++kb) {
           ok = warp_wait(full0 + 8 * stage, phase, abort_flag, p.info, 13, p.wait_ns);
-          if (C::FP4 && CG == 1 && ok) ok = warp_wait(ready0 + 8 * stage, phase, abort_flag, p.info, 16, p.wait_ns);
+          if (C::FP4 && ok) ok = warp_wait(ready0 + 8 * stage, phase, abort_flag, p.info, 16, p.wait_ns);
           if (!ok) break;
           fence_after();
           const uint32_t sb = ring + stage * stage_bytes, sa = sb + C::A_OFF;
           if constexpr (C::FP4) {
             const uint32_t ca = sf0 + stage * C::SF_COLS, cb = ca + 4 * C::ATOMS;
-            if constexpr (CG == 2) {
-              const uint32_t sf = sb + C::B_BYTES;
-#pragma unroll
-              for (int q = 0; q < C::ATOMS; ++q) {
-                copy_scales_pair(on, ca + 4 * q, smem_desc(sf + 512 * q, 128, 128, 0));
-#pragma unroll
-                for (int b = 0; b < C::SFB_TILES; ++b)   // one K tile's columns side by side
-                  copy_scales_pair(on, cb + 4 * (C::SFB_TILES * q + b),
-                                   smem_desc(sf + C::SFA_BYTES + 512 * (C::ATOMS * b + q), 128, 128, 0));
-              }
-            }
             const int n = min(4, p.steps - 4 * kb);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -761,9 +755,48 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
         }
       }
       if (any) {
-        // every MMA and copy this thread issued has completed before TMEM is released
+        // every MMA this thread issued has completed before TMEM is released
         commit_local<CG>(on, drained);
         if (on) mbar_drain(drained, 0);
+      }
+    }
+  } else if (C::FP4 && CG == 2 && warp == C::SCALE_WARP) {
+    // ---------------- scale copies, ahead of the MMAs (the pair's first CTA)
+    if constexpr (C::FP4 && CG == 2) {
+      if (rank == 0) {
+        const uint32_t on = lane == 0;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true, any = false;
+        for (int t = unit0; t < p.num_tiles && ok; t += units) {
+          for (int kb = kb0; kb < kb1; ++kb) {
+            // the buffer's last MMAs are done: the producer waited for them before it filled the stage again
+            ok = warp_wait(full0 + 8 * stage, phase, abort_flag, p.info, 14, p.wait_ns);
+            if (!ok) break;
+            fence_after();
+            const uint32_t sf = ring + stage * stage_bytes + C::B_BYTES;
+            const uint32_t ca = sf0 + stage * C::SF_COLS, cb = ca + 4 * C::ATOMS;
+#pragma unroll
+            for (int q = 0; q < C::ATOMS; ++q) {
+              copy_scales_pair(on, ca + 4 * q, smem_desc(sf + 512 * q, 128, 128, 0));
+#pragma unroll
+              for (int b = 0; b < C::SFB_TILES; ++b)   // one K tile's columns side by side
+                copy_scales_pair(on, cb + 4 * (C::SFB_TILES * q + b),
+                                 smem_desc(sf + C::SFA_BYTES + 512 * (C::ATOMS * b + q), 128, 128, 0));
+            }
+            commit_local<CG>(on, ready0 + 8 * stage);
+            any = true;
+            if (++stage == p.stages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+        if (any) {
+          // every copy this thread issued has completed before TMEM is released
+          commit_local<CG>(on, drained + 8);
+          if (on) mbar_drain(drained + 8, 0);
+        }
       }
     }
   } else {
