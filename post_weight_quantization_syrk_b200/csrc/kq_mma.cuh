@@ -353,6 +353,28 @@ constexpr uint32_t idesc_fp4(bool e8m0, uint32_t M, uint32_t N, uint32_t sf_id) 
          (sf_id << 29);
 }
 
+// 32 lanes x 32 consecutive 32-bit columns, not waited for: ld_wait comes before
+// their use.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// The wait names the registers, so that nothing that reads them moves above it.
+__device__ __forceinline__ void ld_wait32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
 // 32 lanes x 32 consecutive 32-bit columns, waited for.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   uint32_t r[32];
@@ -699,20 +721,36 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
       int stage = 0, buf = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true, any = false;
+      // Whether the coming stage has been seen filled.  A wait costs about 130
+      // cycles even when there is nothing to wait for, and only a few MMAs queue up
+      // behind the issuing thread: looked at between two of a stage's MMAs, the next
+      // stage's barriers cost nothing (925 cycles a stage of 512 MMA cycles without).
+      bool seen = false;
+      auto peek = [&] {
+        const int s1 = stage + 1 == p.stages ? 0 : stage + 1;
+        const uint32_t ph = stage + 1 == p.stages ? phase ^ 1u : phase;
+        seen = test_wait(full0 + 8 * s1, ph);
+        if (C::FP4) seen = seen && test_wait(ready0 + 8 * s1, ph);
+        seen = __all_sync(0xffffffffu, seen);
+      };
       for (int t = unit0; t < p.num_tiles && ok; t += units) {
         if (!warp_wait(accempty0 + 8 * buf, acc_phase ^ 1u, abort_flag, p.info, 12, p.wait_ns)) break;
         const uint32_t d = tmem + buf * C::BN;
         for (int kb = kb0; kb < kb1; ++kb) {
-          ok = warp_wait(full0 + 8 * stage, phase, abort_flag, p.info, 13, p.wait_ns);
-          if (C::FP4 && ok) ok = warp_wait(ready0 + 8 * stage, phase, abort_flag, p.info, 16, p.wait_ns);
-          if (!ok) break;
+          if (!seen) {
+            ok = warp_wait(full0 + 8 * stage, phase, abort_flag, p.info, 13, p.wait_ns);
+            if (C::FP4 && ok) ok = warp_wait(ready0 + 8 * stage, phase, abort_flag, p.info, 16, p.wait_ns);
+            if (!ok) break;
+          }
           fence_after();
           const uint32_t sb = ring + stage * stage_bytes, sa = sb + C::A_OFF;
           if constexpr (C::FP4) {
             const uint32_t ca = sf0 + stage * C::SF_COLS, cb = ca + 4 * C::ATOMS;
             const int n = min(4, p.steps - 4 * kb);
+            if (n <= 2) seen = false;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+              if (j == 2) peek();
               if (j >= n) break;
               const int atom = C::KIND == KIND_MX ? j / 2 : j;
               const uint32_t id = idesc_fp4(C::KIND == KIND_MX, 128 * CG, C::MMA_N, C::KIND == KIND_MX ? 2 * (j & 1) : 0);
@@ -727,6 +765,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
             constexpr uint32_t id = idesc(kFmtBF16, C::AMN, C::BMN, 128 * CG, C::MMA_N);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+              if (j == 2) peek();
               const uint32_t acc = (kb > kb0 || j > 0) ? 1u : 0u;
               const uint64_t da = C::AMN ? smem_desc(sa + 2048 * j, 8192, 1024, kSwizzle128)
                                          : smem_desc(sa + 32 * j, 16, 1024, kSwizzle128);
@@ -853,13 +892,17 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
         if (DRAIN && !p.out_f32) {
           uint4 q[CW / 8];
 #pragma unroll
-          for (int c = 0; c < CW; c += 32) {
-            float v[32];
-            tmem_ld32(d + c, v);
+          for (int c = 0; c < CW; c += 64) {
+            uint32_t w[64];
+            float v[64];
+            tmem_ld32_async(d + c, w);
+            tmem_ld32_async(d + c + 32, w + 32);
+            ld_wait32(w);
+            ld_wait32(w + 32);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= sa;
+            for (int i = 0; i < 64; ++i) v[i] = sa * __uint_as_float(w[i]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) q[c / 8 + k] = pack8(v + 8 * k);
+            for (int k = 0; k < 8; ++k) q[c / 8 + k] = pack8(v + 8 * k);
           }
           release();
 #pragma unroll
