@@ -620,8 +620,9 @@ def _out(t, rows, cols, dtype, like, name, multiple=1):
     rows lie a multiple of `multiple` elements apart."""
     if t is None:
         ld = -(-cols // multiple) * multiple
-        t = like.new_empty((rows, ld), dtype=dtype)
-        return (t if ld == cols else t[:, :cols]), ld
+        if ld == cols:
+            return like.new_empty((rows, cols), dtype=dtype), ld
+        return like.new_empty_strided((rows, cols), (ld, 1), dtype=dtype), ld
     ld = _rows(t, dtype, name)
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must be {[rows, cols]}")

@@ -890,25 +890,22 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
         release();
       } else if constexpr (C::EPI == EPI_STORE) {
         if (DRAIN && !p.out_f32) {
-          uint4 q[CW / 8];
+          // as they are: packing would keep the accumulator 300 cycles longer
+          uint32_t w[CW];
 #pragma unroll
-          for (int c = 0; c < CW; c += 64) {
-            uint32_t w[64];
-            float v[64];
-            tmem_ld32_async(d + c, w);
-            tmem_ld32_async(d + c + 32, w + 32);
-            ld_wait32(w);
-            ld_wait32(w + 32);
+          for (int c = 0; c < CW; c += 32) tmem_ld32_async(d + c, w + c);
 #pragma unroll
-            for (int i = 0; i < 64; ++i) v[i] = sa * __uint_as_float(w[i]);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) q[c / 8 + k] = pack8(v + 8 * k);
-          }
+          for (int c = 0; c < CW; c += 32) ld_wait32(w + c);
           release();
 #pragma unroll
           for (int c = 0; c < CW; c += CH) {
 #pragma unroll
-            for (int k = 0; k < CH / 8; ++k) sts128(piece(stg, lane, k), q[c / 8 + k]);
+            for (int k = 0; k < CH / 8; ++k) {
+              float v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = sa * __uint_as_float(w[c + 8 * k + i]);
+              sts128(piece(stg, lane, k), pack8(v));
+            }
             rows_out<CH / 8>(stg, static_cast<__nv_bfloat16*>(p.out[problem]), p.ldo[problem], r0, p.M, c0 + c, p.N,
                              p.out_vec[problem]);
           }
@@ -942,17 +939,27 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
         }
       } else if constexpr (C::EPI == EPI_GATED) {
         static_assert(CW == CH, "one piece per warp");
-        float g[CH], u[CH];
+        uint32_t wg[CH], wu[CH];
 #pragma unroll
-        for (int h = 0; h < CH; h += 32) tmem_ld32(d + h, g + h);
+        for (int h = 0; h < CH; h += 32) {
+          tmem_ld32_async(d + h, wg + h);
+          tmem_ld32_async(d + C::BN / 2 + h, wu + h);
+        }
 #pragma unroll
-        for (int h = 0; h < CH; h += 32) tmem_ld32(d + C::BN / 2 + h, u + h);
+        for (int h = 0; h < CH; h += 32) {
+          ld_wait32(wg + h);
+          ld_wait32(wu + h);
+        }
         release();
 #pragma unroll
         for (int k = 0; k < CH / 8; ++k) {
+          float v[8];
 #pragma unroll
-          for (int i = 8 * k; i < 8 * k + 8; ++i) g[i] = (sa * g[i]) * gate_of(sa * g[i], p.act).p * (su * u[i]);
-          sts128(piece(stg, lane, k), pack8(g + 8 * k));
+          for (int i = 0; i < 8; ++i) {
+            const float g = sa * __uint_as_float(wg[8 * k + i]);
+            v[i] = g * gate_of(g, p.act).p * (su * __uint_as_float(wu[8 * k + i]));
+          }
+          sts128(piece(stg, lane, k), pack8(v));
         }
         rows_out<CH / 8>(stg, static_cast<__nv_bfloat16*>(p.out[0]), p.ldo[0], r0, p.M, c0, p.N, p.out_vec[0]);
       } else {
@@ -1005,7 +1012,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
   __syncthreads();
   if constexpr (CG == 1) {
     if (p.via_smem) {
-      // sum of the cluster's partials in rank order; each CTA takes a share of the tile's columns
+      // sum of the cluster's partials in rank order; the tile's pieces of 8 columns are dealt to its CTAs
       if (ks > 1) cluster_sync();
       const int problem = unit0 / p.problem_tiles;
       int tm, tn;
@@ -1013,9 +1020,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
       const float sa = (p.ga ? *p.ga : 1.f) * (p.gb[0] ? *p.gb[0] : 1.f);
       const float su = (p.ga ? *p.ga : 1.f) * (p.gb[1] ? *p.gb[1] : 1.f);
       const int rows = (int)min((int64_t)128, p.M - (int64_t)tm * 128);
-      const int cols = C::OUTC / ks;               // a multiple of 8
-      for (int i = threadIdx.x; i < rows * (cols / 8); i += C::THREADS) {
-        const int rr = i / (cols / 8), c = (int)crank * cols + 8 * (i % (cols / 8));
+      for (int i = threadIdx.x + C::THREADS * (int)crank; i < rows * (C::OUTC / 8); i += C::THREADS * ks) {
+        const int rr = i / (C::OUTC / 8), c = 8 * (i % (C::OUTC / 8));
         const uint32_t at = ring + 4u * (uint32_t)(rr * C::PART_LD + c);
         float a[8], u[8];
 #pragma unroll
@@ -1081,7 +1087,8 @@ struct Cost {
 // many as the SMs (11008 x 4096, 16 rows, MX: 9.9 us with 172 CTAs, 11.4 with 86, 15.4
 // with 344).  Above, the cheaper by the sums above (1024 x 4096 x 4096: 15.7 us on 64
 // pairs, 22.4 on 256 tiles; 512 rows: 14.8 on 32 pairs, 11.5 on 128 tiles; 333 x 1001 x
-// 5460: 16.4 us with K over 4 CTAs, 30.0 without).
+// 5460: 16.4 us with K over 4 CTAs, 30.0 without).  Clusters are powers of two: of 5 or
+// 6 CTAs fewer fit the GPU at a time (64 x 4096 x 4096: 19.7 us over 5, 11.1 over 4).
 inline Plan make_plan(int64_t M, int64_t slim, int64_t pairs, int64_t stages, Cost c) {
   constexpr int64_t kSms = 148, kPairs = 74;
   if (M <= 64) {
