@@ -395,13 +395,11 @@ __device__ __forceinline__ void load_x(const __nv_bfloat16* x, int64_t k, int64_
 // truncation, 8 bits each: exact.  A value without a finite remainder (NaN, Inf)
 // is its first part alone.
 __device__ __forceinline__ void split3(float x, uint32_t (&part)[3]) {
-  part[0] = __float_as_uint(x);
-  if ((part[0] & 0x7f800000u) == 0x7f800000u) {
-    if (part[0] & 0x7fffffu) part[0] |= 0x400000u;   // a NaN whose top bits are zero stays one
-    part[1] = part[2] = 0;
-    return;
-  }
-  const float r1 = x - __uint_as_float(part[0] & 0xffff0000u);
+  const uint32_t bits = __float_as_uint(x);
+  const bool finite = (bits & 0x7f800000u) != 0x7f800000u;
+  // a NaN whose top bits are zero stays one
+  part[0] = x != x ? bits | 0x400000u : bits;
+  const float r1 = finite ? x - __uint_as_float(bits & 0xffff0000u) : 0.f;
   part[1] = __float_as_uint(r1);
   part[2] = __float_as_uint(r1 - __uint_as_float(part[1] & 0xffff0000u));
 }
