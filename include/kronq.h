@@ -539,13 +539,16 @@ kq_status kq_reverted_matvec(const uint32_t* packed, int64_t d_out, int64_t d_in
  *   positive and finite (KQ_ERR_INVALID_ARG).  M_hat must not overlap M.
  * kq_fp4_gemm: Y [A->rows, B->rows] = A B^T (same format and columns), dtype
  *   KQ_F32 or KQ_BF16, ldy >= B->rows.  Block-scaled tensor-core products,
- *   fp32 sums.  Any number of rows from 0; `info`: KQ_ERR_TIMEOUT.
+ *   fp32 sums (the tensor core truncates: up to 2^-24 of a sum per 64 columns).
+ *   Any number of rows from 0, at most 2^20 columns (2^24 tiles of 128 x 64 of
+ *   Y); Y must not overlap the operands; `info`: KQ_ERR_TIMEOUT.
  * kq_fp4_matvec: Y[b, :] = W X[b, :] for b < batch (1..8) with unquantised
  *   vectors, the single-token form of the product: X [batch, W->cols] and Y
  *   [batch, W->rows] both of `dtype` (KQ_F32 or KQ_BF16), fp32 sums.
  * kq_fp4_gated_ffn: H [X->rows, f] = act(X W_gate^T) * (X W_up^T), bf16, over
  *   4-bit X [T, d] and weights [f, d] of one format: both projections, the
- *   activation and the product in one kernel (see kq_gated_ffn).
+ *   activation and the product in one kernel (see kq_gated_ffn).  Limits as
+ *   kq_fp4_gemm.
  * ------------------------------------------------------------------------ */
 enum { KQ_F32 = 0, KQ_BF16 = 1 };
 enum { KQ_FP4_MX = 0, KQ_FP4_NV = 1 };
@@ -587,8 +590,9 @@ kq_status kq_fp4_gated_ffn(const kq_fp4* X, const kq_fp4* W_gate, const kq_fp4* 
  *   tensors aligned to their elements.  No output may overlap an input or
  *   another output.  tokens == 0: the weights' gradients are zeros, the other
  *   tensors may be NULL.
- * All bf16 as uint16_t bit patterns.  Limits: 0 <= tokens <= 2^24, 1 <= d, f <=
- * 2^20.  `info`: KQ_ERR_TIMEOUT.  NaN and Inf propagate.
+ * All bf16 as uint16_t bit patterns.  Limits: 0 <= tokens <= 2^24 (2^18 with
+ * dW_gate, dW_up: add the gradients of several calls beyond), 1 <= d, f <= 2^17.
+ * `info`: KQ_ERR_TIMEOUT.  NaN and Inf propagate.
  * ------------------------------------------------------------------------ */
 kq_status kq_gated_ffn(const uint16_t* X, int64_t tokens, int64_t d, int64_t ldx, const uint16_t* W_gate,
                        const uint16_t* W_up, int64_t f, int64_t ldw, int act, uint16_t* H, int64_t ldh,

@@ -66,8 +66,8 @@ kq_status gated(const char* what, const Shape& s, const uint16_t* X, int64_t ldx
 kq_status check(const char* what, const Shape& s, const uint16_t* X, int64_t ldx, const uint16_t* Wg, const uint16_t* Wu,
                 int64_t ldw, int act, const int32_t* info) {
   if (s.T < 0 || s.d < 1 || s.f < 1) return kq::fail(KQ_ERR_INVALID_ARG, "%s: need tokens >= 0, d >= 1, f >= 1", what);
-  if (s.T > (1 << 24) || s.d > (1 << 20) || s.f > (1 << 20))
-    return kq::fail(KQ_ERR_UNSUPPORTED_SHAPE, "%s: tokens above 2^24, or d or f above 2^20", what);
+  if (s.T > (1 << 24) || s.d > (1 << 17) || s.f > (1 << 17))
+    return kq::fail(KQ_ERR_UNSUPPORTED_SHAPE, "%s: tokens above 2^24, or d or f above 2^17", what);
   if (kq::cdiv(s.T, 128) * kq::cdiv(std::max(s.d, s.f), 64) > (1 << 24))
     return kq::fail(KQ_ERR_UNSUPPORTED_SHAPE, "%s: more than 2^24 tiles of 128 x 64", what);
   if (act != KQ_ACT_SILU && act != KQ_ACT_GELU) return kq::fail(KQ_ERR_INVALID_ARG, "%s: unknown activation", what);
@@ -114,6 +114,11 @@ extern "C" kq_status kq_gated_ffn_backward(const uint16_t* X, int64_t tokens, in
   const Shape s = {tokens, d, f};
   KQ_TRY(check(what, s, X, ldx, W_gate, W_up, ldw, act, info));
   if (!dW_gate != !dW_up) return kq::fail(KQ_ERR_INVALID_ARG, "%s: dW_gate and dW_up go together", what);
+  // The tensor core truncates as it accumulates, up to 2^-24 of the sum per MMA of 16
+  // terms: a sum over 2^18 terms (tokens; or 2 f for dX) loses at most 2^-10, half of
+  // what rounding it to bf16 may.
+  if (dW_gate && tokens > (1 << 18))
+    return kq::fail(KQ_ERR_UNSUPPORTED_SHAPE, "%s: weights' gradients of more than 2^18 tokens (call it per batch and add)", what);
   if (tokens > 0 && (!dH || !dG || !dU)) return kq::fail(KQ_ERR_INVALID_ARG, "%s: NULL pointer", what);
   if (lddh < f || ldg < f || (H && ldh < f) || (dX && lddx < d) || (dW_gate && lddw < d))
     return kq::fail(KQ_ERR_INVALID_ARG, "%s: leading dimension too small", what);

@@ -34,6 +34,8 @@ inline kq_status check(const kq_fp4* q, const char* what, const char* name) {
   if (q->rows < 0 || q->cols < 1) return fail(KQ_ERR_INVALID_ARG, "%s: %s needs rows >= 0 and cols >= 1", what, name);
   if (q->rows > (1 << 30) || q->cols > (1 << 24))
     return fail(KQ_ERR_UNSUPPORTED_SHAPE, "%s: %s above 2^30 rows or 2^24 columns", what, name);
+  if (cdiv(q->rows, 128) * scale_tiles(q->cols, q->format) > 0x7fffffff)   // TMA coordinates are 32 bits
+    return fail(KQ_ERR_UNSUPPORTED_SHAPE, "%s: %s has more than 2^31 - 1 scale tiles", what, name);
   if (q->rows > 0 && (!q->codes || !q->scales)) return fail(KQ_ERR_INVALID_ARG, "%s: %s has a NULL pointer", what, name);
   if (q->ld < cdiv(q->cols, 32) * 16) return fail(KQ_ERR_INVALID_ARG, "%s: %s leading dimension too small", what, name);
   if (!aligned(q->codes, 16) || !aligned(q->scales, 16) || (q->ld & 15) || !aligned(q->gscale, 4))

@@ -61,6 +61,10 @@ kq_status choose(const char* what, const kq_fp4* A, const kq_fp4* B0, const kq_f
   return run<Slim<KIND, EPI>>(what, A, B0, B1, p, plan.ks, st);
 }
 
+// Longest K: the tensor core truncates as it accumulates, up to 2^-24 of the sum per
+// MMA of 64 columns, so that a longer chain would lose more than bf16 rounding does.
+constexpr int64_t kMaxCols = 1 << 20;
+
 }  // namespace
 
 extern "C" kq_status kq_fp4_gemm(const kq_fp4* A, const kq_fp4* B, void* Y, int dtype, int64_t ldy, int32_t* info,
@@ -69,6 +73,7 @@ extern "C" kq_status kq_fp4_gemm(const kq_fp4* A, const kq_fp4* B, void* Y, int 
   KQ_TRY(kq::fp4::check(B, "kq_fp4_gemm", "B"));
   if (A->format != B->format || A->cols != B->cols)
     return kq::fail(KQ_ERR_INVALID_ARG, "kq_fp4_gemm: A and B need the same format and columns");
+  if (A->cols > kMaxCols) return kq::fail(KQ_ERR_UNSUPPORTED_SHAPE, "kq_fp4_gemm: more than 2^20 columns");
   if (dtype != KQ_F32 && dtype != KQ_BF16) return kq::fail(KQ_ERR_INVALID_ARG, "kq_fp4_gemm: dtype must be KQ_F32 or KQ_BF16");
   if (!info) return kq::fail(KQ_ERR_INVALID_ARG, "kq_fp4_gemm: NULL pointer");
   if (A->rows == 0 || B->rows == 0) {
@@ -109,6 +114,7 @@ extern "C" kq_status kq_fp4_gated_ffn(const kq_fp4* X, const kq_fp4* W_gate, con
   if (X->format != W_gate->format || X->format != W_up->format || X->cols != W_gate->cols || X->cols != W_up->cols ||
       W_gate->rows != W_up->rows)
     return kq::fail(KQ_ERR_INVALID_ARG, "kq_fp4_gated_ffn: X, W_gate and W_up need the same format and columns, the weights the same rows");
+  if (X->cols > kMaxCols) return kq::fail(KQ_ERR_UNSUPPORTED_SHAPE, "kq_fp4_gated_ffn: more than 2^20 columns");
   if (act != KQ_ACT_SILU && act != KQ_ACT_GELU) return kq::fail(KQ_ERR_INVALID_ARG, "kq_fp4_gated_ffn: unknown activation");
   if (!info) return kq::fail(KQ_ERR_INVALID_ARG, "kq_fp4_gated_ffn: NULL pointer");
   if (X->rows == 0 || W_gate->rows == 0) {

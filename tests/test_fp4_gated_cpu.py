@@ -76,6 +76,10 @@ def test_product_refusals():
     assert L.kq_fp4_gemm(a, a, A, P.KQ_F32, 15, A, None) == 1
     assert L.kq_fp4_gemm(a, a, A, P.KQ_F32, 16, None, None) == 1
     assert L.kq_fp4_gemm(a, a, A + 2, P.KQ_F32, 16, A, None) == 3
+    assert L.kq_fp4_gemm(mat(cols=(1 << 20) + 1), mat(cols=(1 << 20) + 1), A, P.KQ_F32, 16, A, None) == 2
+    w = mat(cols=(1 << 20) + 1)
+    assert L.kq_fp4_gated_ffn(w, w, w, 0, A, 16, A, None) == 2
+    assert L.kq_fp4_matvec(mat(rows=1 << 30, cols=1 << 24), A, P.KQ_F32, 1 << 24, 1, A, 1 << 30, None) == 2   # scale tiles
     huge = mat(rows=1 << 22)
     assert L.kq_fp4_gemm(huge, huge, A, P.KQ_F32, 1 << 22, A, None) == 2
     assert L.kq_fp4_gemm(mat(rows=0), a, None, P.KQ_F32, 16, A, None) == 0
@@ -118,7 +122,8 @@ def backward(X=A, T=16, d=64, ldx=64, wg=A, wu=A, f=32, ldw=64, act=0, dH=A, ldd
     (dict(X=None), 1), (dict(wg=None), 1), (dict(wu=None), 1), (dict(info=None), 1), (dict(T=-1), 1), (dict(d=0), 1),
     (dict(f=0), 1), (dict(ldx=63), 1), (dict(ldw=63), 1), (dict(act=-1), 1), (dict(act=2), 1), (dict(ldx=68), 3),
     (dict(ldw=68), 3), (dict(X=A + 8), 3), (dict(wg=A + 2), 3), (dict(wu=A + 4), 3), (dict(T=(1 << 24) + 1), 2),
-    (dict(d=(1 << 20) + 1, ldx=1 << 21, ldw=1 << 21), 2), (dict(T=1 << 24, f=1 << 20, ldh=1 << 20), 2)])
+    (dict(d=(1 << 17) + 1, ldx=1 << 21, ldw=1 << 21), 2), (dict(f=(1 << 17) + 1, ldh=1 << 21), 2),
+    (dict(T=1 << 24, f=1 << 17, ldh=1 << 17), 2)])
 def test_gated_refusals(fn, kw, status):
     if fn is backward:
         kw = {k: v for k, v in kw.items() if k != "ldh"}
@@ -142,6 +147,7 @@ def test_gated_output_refusals():
     assert backward(dWg=A, dWu=A, lddw=63) == 1
     assert backward(dWg=A, lddw=64) == 1 and b"go together" in lib().kq_last_error()
     assert backward(dX=A + 1, lddx=64) == 3
+    assert backward(T=(1 << 18) + 1, dWg=A, dWu=A, lddw=64) == 2 and b"2^18" in lib().kq_last_error()
     assert backward(T=0, X=None, dH=None, dG=None, dU=None) == 0      # no weights' gradients asked: nothing to do
 
 

@@ -356,6 +356,40 @@ def test_wrong_shapes_are_refused(P):
         P.Fp4Matrix(8, 64, P.KQ_FP4_MX, A.codes, A.scales[:256])
 
 
+@pytest.mark.slow
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_offsets_past_32_bits(P, fmt):
+    """70016 x 65536: codes past 2^31 bytes, M past 2^32: the last rows as on their own."""
+    rows, cols, tail = 70016, 65536, 128
+    M = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    M[-tail:] = _data(5, tail, cols, torch.bfloat16)
+    g = _g(M[-tail:]) if fmt == "nv" else None
+    Q = P.kq_fp4_quantize(M, _fmt(P, fmt), g)
+    last = P.kq_fp4_quantize(M[-tail:], _fmt(P, fmt), g)
+    del M
+    assert torch.equal(Q.codes[-tail:], last.codes) and torch.equal(Q.scales[-last.scales.numel():], last.scales)
+    assert int(Q.codes[:tail].sum()) == 0
+    X = _data(6, 3, cols, torch.bfloat16)
+    assert torch.equal(P.kq_fp4_matvec(Q, X)[:, -tail:], P.kq_fp4_matvec(last, X))
+    B = _quant(P, _data(7, 64, cols), fmt)
+    Y, Z = P.kq_fp4_gemm(Q, B), P.kq_fp4_gemm(last, B)
+    # one chain over K or several: within the sums' bound
+    tol = 2.0 ** -7 * Z.float().abs() + 2.0 ** -23 * cols * float(Z.float().abs().max()) / 100
+    assert bool(((Y[-tail:].float() - Z.float()).abs() <= tol).all()) and int((Y[:-tail] != 0).sum()) == 0
+
+
+@pytest.mark.slow
+def test_long_products_keep_their_sums(P):
+    """131072 columns of one sign, where truncation adds up: within its bound."""
+    k = 131072
+    A = P.kq_fp4_quantize(torch.rand((40, k), device="cuda") + 0.5, P.KQ_FP4_MX)
+    B = P.kq_fp4_quantize(torch.rand((200, k), device="cuda") + 0.5, P.KQ_FP4_MX)
+    ref = _values(A, "mx") @ _values(B, "mx").T
+    Y = np64(P.kq_fp4_gemm(A, B, dtype=torch.float32))
+    # k / 64 MMAs, each up to 2^-24 of the sum so far (twice for the alignment of its terms)
+    assert np.abs(Y / ref - 1).max() <= 2 * k / 64 * 2.0 ** -24
+
+
 # ------------------------------------------------------------ together
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])

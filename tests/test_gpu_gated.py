@@ -224,6 +224,23 @@ def test_streams_and_graph(P):
         assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
+@pytest.mark.slow
+def test_offsets_past_32_bits(P):
+    """40000 tokens x 60000 features: H, dG and dU past 2^31 elements; the last rows as on their own."""
+    t, d, f, tail = 40000, 64, 60000, 130
+    rng = np.random.default_rng(1)
+    X, Wg, Wu = _mat(rng, t, d), _mat(rng, f, d, 0.1), _mat(rng, f, d, 0.1)
+    dH = torch.ones((t, f), dtype=torch.bfloat16, device="cuda")
+    H = P.kq_gated_ffn(X, Wg, Wu, 0)
+    assert torch.equal(H[-tail:], P.kq_gated_ffn(X[-tail:], Wg, Wu, 0))
+    dG, dU, dX, _, _ = P.kq_gated_ffn_backward(X, Wg, Wu, dH, 0, H=H, need_dW=False)
+    want = P.kq_gated_ffn_backward(X[-tail:], Wg, Wu, dH[-tail:], 0, need_dW=False)
+    assert torch.equal(dG[-tail:], want[0]) and torch.equal(dU[-tail:], want[1])
+    # dX: one chain over K or several
+    a, b = dX[-tail:].float(), want[2].float()
+    assert bool(((a - b).abs() <= 2.0 ** -7 * b.abs() + 1e-3 * float(b.abs().max())).all())
+
+
 @pytest.mark.parametrize("t", [40, 2304])
 def test_expired_wait_is_reported(P, t):
     X, Wg, Wu, _ = _block(21, t, 2048, 1024)
