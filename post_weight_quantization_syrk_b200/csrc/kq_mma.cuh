@@ -81,8 +81,7 @@ struct Cfg {
   static constexpr int TMEM_COLS = COLS <= 64 ? 64 : (COLS <= 128 ? 128 : (COLS <= 256 ? 256 : 512));
   static constexpr int EW = 8;                               // epilogue warps
   static constexpr int EW0 = 2;                              // the first of them
-  static constexpr int SCALE_WARP = EW0 + EW;                // of a pair
-  static constexpr int THREADS = 32 * (EW0 + EW + (FP4 && CG == 2 ? 1 : 0));
+  static constexpr int THREADS = 32 * (EW0 + EW);
   static constexpr int PART_LD = BN + 4;                     // row stride of the split-K partials
   static constexpr int RING = STAGES * (A_OFF + A_BYTES);    // at most: stages shrink with A's box, and p.stages may be fewer
   static constexpr int STAGING = EW * 4096;                  // 32 rows x 128 bytes per epilogue warp
@@ -205,27 +204,28 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return ok && __all_sync(0xffffffffu, try_wait(bar, parity));   // every lane acquires
 }
 
-// The issuing warps run their loops as whole warps and predicate only the
-// tcgen05 and TMA instructions on one lane (`on`): their operands then stay in
-// uniform registers, as the instructions want them.
+// The lane of a warp that issues its tcgen05 and TMA instructions (always the same
+// one).  The issuing warps run their loops as whole warps and branch on this around
+// a stage's instructions: the compiler then knows that one thread is left and
+// issues them back to back.  Instructions predicated on a lane number instead cost
+// some 80 cycles each (MX pairs, a stage of 10: 0.56 us, here 0.40).
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+  return r != 0;
+}
 
 // A TMA tile load; with CG = 2 the barrier may be the pair leader's.
 template <int CG>
-__device__ __forceinline__ void load_2d(uint32_t on, uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   if constexpr (CG == 2)
     asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-        "[%4];\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(on)
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
   else
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(
-            dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(on)
-        : "memory");
+    tma_load_2d(dst, map, x, y, bar);
 }
 
 template <int CG, int NCOLS>
@@ -247,40 +247,33 @@ __device__ __forceinline__ void free_tmem(uint32_t taddr) {
 
 // Arrive on `bar` (of both CTAs of a pair) once the MMAs and copies issued so far are done.
 template <int CG>
-__device__ __forceinline__ void commit(uint32_t on, uint32_t bar) {
+__device__ __forceinline__ void commit(uint32_t bar) {
   if constexpr (CG == 2)
     asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
-        "h"((uint16_t)3), "r"(on)
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
         : "memory");
   else
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(on)
-        : "memory");
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // The same on this CTA's barrier alone.
 template <int CG>
-__device__ __forceinline__ void commit_local(uint32_t on, uint32_t bar) {
+__device__ __forceinline__ void commit_local(uint32_t bar) {
   if constexpr (CG == 2)
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(on)
-        : "memory");
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
   else
-    commit<1>(on, bar);
+    commit<1>(bar);
 }
 
 #define KQ_MMA_BF16(CGN)                                                                                             \
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"                          \
-               "@q tcgen05.mma.cta_group::" CGN ".kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),                     \
-               "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on)                                                         \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                                     \
+               "tcgen05.mma.cta_group::" CGN ".kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),                        \
+               "l"(a), "l"(b), "r"(idesc), "r"(acc)                                                                  \
                : "memory")
 
 template <int CG>
-__device__ __forceinline__ void mma_bf16(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   if constexpr (CG == 2)
     KQ_MMA_BF16("2");
   else
@@ -288,14 +281,14 @@ __device__ __forceinline__ void mma_bf16(uint32_t on, uint32_t d, uint64_t a, ui
 }
 
 #define KQ_MMA_FP4(CGN, KINDVEC)                                                                                     \
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"                          \
-               "@q tcgen05.mma.cta_group::" CGN "." KINDVEC " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),         \
-               "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc), "r"(on)                                      \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                                     \
+               "tcgen05.mma.cta_group::" CGN "." KINDVEC " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),          \
+               "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)                                              \
                : "memory")
 
 template <int KIND, int CG>
-__device__ __forceinline__ void mma_fp4(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                        uint32_t sfb, uint32_t acc) {
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                        uint32_t acc) {
   if constexpr (KIND == KIND_MX && CG == 1) KQ_MMA_FP4("1", "kind::mxf4.block_scale.scale_vec::2X");
   if constexpr (KIND == KIND_MX && CG == 2) KQ_MMA_FP4("2", "kind::mxf4.block_scale.scale_vec::2X");
   if constexpr (KIND == KIND_NV && CG == 1) KQ_MMA_FP4("1", "kind::mxf4nvf4.block_scale.scale_vec::4X");
@@ -329,11 +322,8 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* v) {
 
 // One 512-byte scale tile to 4 TMEM columns, repeated in the four lane quarters
 // of both CTAs of a pair.
-__device__ __forceinline__ void copy_scales_pair(uint32_t on, uint32_t taddr, uint64_t desc) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-      "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(desc), "r"(on)
-      : "memory");
+__device__ __forceinline__ void copy_scales_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -582,8 +572,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
   // bars: full [0, S), empty [S, 2S), scales landed [2S, 3S), scales in TMEM
   // [3S, 4S), acc full [4S, 4S + 2), acc empty [4S + 2, 4S + 4), MMAs drained
-  // [4S + 4], scale copies drained [4S + 5]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * S + 6);
+  // [4S + 4]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * S + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S, landed0 = full0 + 16 * S, ready0 = full0 + 24 * S;
   const uint32_t accfull0 = full0 + 32 * S, accempty0 = accfull0 + 16, drained = accfull0 + 32;
@@ -603,14 +593,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
       mbar_init(landed0 + 8 * s, 1);
-      mbar_init(ready0 + 8 * s, CG == 2 ? 1 : 4);
+      mbar_init(ready0 + 8 * s, 4);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accfull0 + 8 * b, 1);
       mbar_init(accempty0 + 8 * b, CG * C::EW);
     }
     mbar_init(drained, 1);
-    mbar_init(drained + 8, 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
@@ -644,7 +633,6 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
 
   if (warp == 0) {
     // ---------------- TMA producer
-    const uint32_t on = lane == 0;
     int stage = 0;
     uint32_t phase = 0, issued_phase = 0, issued = 0;   // bit s: stage s
     bool ok = true;
@@ -659,41 +647,44 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
           ok = false;
           break;
         }
-        uint32_t fb = full0 + 8 * stage;
-        if (on && rank == 0) mbar_arrive_expect_tx(fb, stage_tx);
-        if (CG == 2) fb = mapa(fb, 0);
-        const uint32_t sb = ring + stage * stage_bytes, sa = sb + C::A_OFF;
-        const int seg = kb >= p.seg_blocks, k = kb - (seg ? p.seg_blocks : 0);
-        const CUtensorMap* ma = &maps.a[problem ? 1 : seg];
-        const CUtensorMap* mb = &maps.b[seg];
-        constexpr int KE = C::FP4 ? 128 : 64;   // map elements per stage along K (bytes of codes, or bf16)
-        if constexpr (C::FP4) {
-          const uint32_t sf = sb + C::B_BYTES, lb = CG == 2 ? fb : landed0 + 8 * stage;
-          if (CG == 1 && on) mbar_arrive_expect_tx(lb, C::SFA_BYTES + C::SFB_BYTES);
-          load_2d<CG>(on, sf, &maps.sfa, 0, (m0 / 128) * p.kat + kb * C::ATOMS, lb);
+        if (elect()) {
+          uint32_t fb = full0 + 8 * stage;
+          if (rank == 0) mbar_arrive_expect_tx(fb, stage_tx);
+          if (CG == 2) fb = mapa(fb, 0);
+          const uint32_t sb = ring + stage * stage_bytes, sa = sb + C::A_OFF;
+          const int seg = kb >= p.seg_blocks, k = kb - (seg ? p.seg_blocks : 0);
+          const CUtensorMap* ma = &maps.a[problem ? 1 : seg];
+          const CUtensorMap* mb = &maps.b[seg];
+          constexpr int KE = C::FP4 ? 128 : 64;   // map elements per stage along K (bytes of codes, or bf16)
+          if constexpr (C::FP4) {
+            const uint32_t sf = sb + C::B_BYTES, lb = CG == 2 ? fb : landed0 + 8 * stage;
+            if (CG == 1) mbar_arrive_expect_tx(lb, C::SFA_BYTES + C::SFB_BYTES);
+            load_2d<CG>(sf, &maps.sfa, 0, (m0 / 128) * p.kat + kb * C::ATOMS, lb);
 #pragma unroll
-          for (int q = 0; q < C::SFB_TILES; ++q)
-            load_2d<CG>(on, sf + C::SFA_BYTES * (1 + q), C::DUAL ? &maps.sfb[q] : &maps.sfb[0], 0,
-                       (n0 / 128 + (C::DUAL ? 0 : q)) * p.kat + kb * C::ATOMS, lb);
-        }
-        if constexpr (C::AMN) {
-          load_2d<CG>(on, sa, ma, m0, 64 * k, fb);
-          load_2d<CG>(on, sa + 8192, ma, m0 + 64, 64 * k, fb);
-        } else {
-          load_2d<CG>(on, sa, ma, KE * k, m0, fb);
-        }
-        if constexpr (C::BMN) {
+            for (int q = 0; q < C::SFB_TILES; ++q)
+              load_2d<CG>(sf + C::SFA_BYTES * (1 + q), C::DUAL ? &maps.sfb[q] : &maps.sfb[0], 0,
+                         (n0 / 128 + (C::DUAL ? 0 : q)) * p.kat + kb * C::ATOMS, lb);
+          }
+          if constexpr (C::AMN) {
+            load_2d<CG>(sa, ma, m0, 64 * k, fb);
+            load_2d<CG>(sa + 8192, ma, m0 + 64, 64 * k, fb);
+          } else {
+            load_2d<CG>(sa, ma, KE * k, m0, fb);
+          }
+          if constexpr (C::BMN) {
 #pragma unroll
-          for (int q = 0; q < C::BN / CG / 64; ++q)
-            load_2d<CG>(on, sb + 8192 * q, mb, n0 + (int)rank * (C::BN / CG) + 64 * q, 64 * k, fb);
-        } else if constexpr (C::DUAL && CG == 2) {
-          load_2d<CG>(on, sb, &maps.b[rank], KE * k, n0, fb);
-        } else if constexpr (C::DUAL) {
-          load_2d<CG>(on, sb, &maps.b[0], KE * k, n0, fb);
-          load_2d<CG>(on, sb + C::MMA_N * 128, &maps.b[1], KE * k, n0, fb);
-        } else {
-          load_2d<CG>(on, sb, mb, KE * k, n0 + (int)rank * (C::BN / CG), fb);
+            for (int q = 0; q < C::BN / CG / 64; ++q)
+              load_2d<CG>(sb + 8192 * q, mb, n0 + (int)rank * (C::BN / CG) + 64 * q, 64 * k, fb);
+          } else if constexpr (C::DUAL && CG == 2) {
+            load_2d<CG>(sb, &maps.b[rank], KE * k, n0, fb);
+          } else if constexpr (C::DUAL) {
+            load_2d<CG>(sb, &maps.b[0], KE * k, n0, fb);
+            load_2d<CG>(sb + C::MMA_N * 128, &maps.b[1], KE * k, n0, fb);
+          } else {
+            load_2d<CG>(sb, mb, KE * k, n0 + (int)rank * (C::BN / CG), fb);
+          }
         }
+        __syncwarp();
         issued |= 1u << stage;
         issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
         if (++stage == p.stages) {
@@ -717,77 +708,72 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
   } else if (warp == 1) {
     // ---------------- MMA issuer (the pair's first CTA)
     if (rank == 0) {
-      const uint32_t on = lane == 0;
       int stage = 0, buf = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true, any = false;
-      // Whether the coming stage has been seen filled.  A wait costs about 130
-      // cycles even when there is nothing to wait for, and only a few MMAs queue up
-      // behind the issuing thread: looked at between two of a stage's MMAs, the next
-      // stage's barriers cost nothing (925 cycles a stage of 512 MMA cycles without).
-      bool seen = false;
-      auto peek = [&] {
-        const int s1 = stage + 1 == p.stages ? 0 : stage + 1;
-        const uint32_t ph = stage + 1 == p.stages ? phase ^ 1u : phase;
-        seen = test_wait(full0 + 8 * s1, ph);
-        if (C::FP4) seen = seen && test_wait(ready0 + 8 * s1, ph);
-        seen = __all_sync(0xffffffffu, seen);
-      };
       for (int t = unit0; t < p.num_tiles && ok; t += units) {
         if (!warp_wait(accempty0 + 8 * buf, acc_phase ^ 1u, abort_flag, p.info, 12, p.wait_ns)) break;
         const uint32_t d = tmem + buf * C::BN;
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!seen) {
-            ok = warp_wait(full0 + 8 * stage, phase, abort_flag, p.info, 13, p.wait_ns);
-            if (C::FP4 && ok) ok = warp_wait(ready0 + 8 * stage, phase, abort_flag, p.info, 16, p.wait_ns);
-            if (!ok) break;
-          }
+          ok = warp_wait(full0 + 8 * stage, phase, abort_flag, p.info, 13, p.wait_ns);
+          if (C::FP4 && CG == 1 && ok) ok = warp_wait(ready0 + 8 * stage, phase, abort_flag, p.info, 16, p.wait_ns);
+          if (!ok) break;
           fence_after();
           const uint32_t sb = ring + stage * stage_bytes, sa = sb + C::A_OFF;
-          if constexpr (C::FP4) {
-            const uint32_t ca = sf0 + stage * C::SF_COLS, cb = ca + 4 * C::ATOMS;
-            const int n = min(4, p.steps - 4 * kb);
-            if (n <= 2) seen = false;
+          if (elect()) {
+            if constexpr (C::FP4) {
+              const uint32_t ca = sf0 + stage * C::SF_COLS, cb = ca + 4 * C::ATOMS;
+              const uint64_t da = smem_desc(sa, 16, 1024, kSwizzle128), db = smem_desc(sb, 16, 1024, kSwizzle128);
+              const uint64_t sf = smem_desc(sb + C::B_BYTES, 128, 128, 0);   // addresses count 16 bytes
+              const int n = min(4, p.steps - 4 * kb);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (j == 2) peek();
-              if (j >= n) break;
-              const int atom = C::KIND == KIND_MX ? j / 2 : j;
-              const uint32_t id = idesc_fp4(C::KIND == KIND_MX, 128 * CG, C::MMA_N, C::KIND == KIND_MX ? 2 * (j & 1) : 0);
-              const uint32_t acc = (kb > kb0 || j > 0) ? 1u : 0u;
+              for (int j = 0; j < 4; ++j) {
+                if (j >= n) break;
+                const int atom = C::KIND == KIND_MX ? j / 2 : j;
+                if constexpr (CG == 2) {
+                  if (C::KIND == KIND_NV || j % 2 == 0) {
+                    // the buffer's last MMAs are done: the producer waited for them before it filled the stage again
+                    copy_scales_pair(ca + 4 * atom, sf + 32 * atom);
 #pragma unroll
-              for (int s = 0; s < C::NSUB; ++s)
-                mma_fp4<C::KIND, CG>(on, d + s * C::MMA_N, smem_desc(sa + 32 * j, 16, 1024, kSwizzle128),
-                                     smem_desc(sb + s * C::MMA_N * 128 + 32 * j, 16, 1024, kSwizzle128), id,
-                                     ca + 4 * atom, cb + C::SFB_W * (C::SFB_TILES * atom + s), acc);
-            }
-          } else {
-            constexpr uint32_t id = idesc(kFmtBF16, C::AMN, C::BMN, 128 * CG, C::MMA_N);
+                    for (int b = 0; b < C::SFB_TILES; ++b)   // one K tile's columns side by side
+                      copy_scales_pair(cb + 4 * (C::SFB_TILES * atom + b), sf + 32 * (C::ATOMS * (1 + b) + atom));
+                  }
+                }
+                const uint32_t id = idesc_fp4(C::KIND == KIND_MX, 128 * CG, C::MMA_N, C::KIND == KIND_MX ? 2 * (j & 1) : 0);
+                const uint32_t acc = (kb > kb0 || j > 0) ? 1u : 0u;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (j == 2) peek();
-              const uint32_t acc = (kb > kb0 || j > 0) ? 1u : 0u;
-              const uint64_t da = C::AMN ? smem_desc(sa + 2048 * j, 8192, 1024, kSwizzle128)
-                                         : smem_desc(sa + 32 * j, 16, 1024, kSwizzle128);
+                for (int s = 0; s < C::NSUB; ++s)
+                  mma_fp4<C::KIND, CG>(d + s * C::MMA_N, da + 2 * j, db + s * C::MMA_N * 8 + 2 * j, id, ca + 4 * atom,
+                                       cb + C::SFB_W * (C::SFB_TILES * atom + s), acc);
+              }
+            } else {
+              constexpr uint32_t id = idesc(kFmtBF16, C::AMN, C::BMN, 128 * CG, C::MMA_N);
 #pragma unroll
-              for (int s = 0; s < C::NSUB; ++s) {
-                const uint32_t bs = sb + s * C::MMA_N * 128;
-                mma_bf16<CG>(on, d + s * C::MMA_N, da,
-                             C::BMN ? smem_desc(bs + 2048 * j, 8192, 1024, kSwizzle128)
-                                    : smem_desc(bs + 32 * j, 16, 1024, kSwizzle128),
-                             id, acc);
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t acc = (kb > kb0 || j > 0) ? 1u : 0u;
+                const uint64_t da = C::AMN ? smem_desc(sa + 2048 * j, 8192, 1024, kSwizzle128)
+                                           : smem_desc(sa + 32 * j, 16, 1024, kSwizzle128);
+#pragma unroll
+                for (int s = 0; s < C::NSUB; ++s) {
+                  const uint32_t bs = sb + s * C::MMA_N * 128;
+                  mma_bf16<CG>(d + s * C::MMA_N, da,
+                               C::BMN ? smem_desc(bs + 2048 * j, 8192, 1024, kSwizzle128)
+                                      : smem_desc(bs + 32 * j, 16, 1024, kSwizzle128),
+                               id, acc);
+                }
               }
             }
+            commit<CG>(empty0 + 8 * stage);   // the stage is free once these MMAs have read it
           }
+          __syncwarp();
           any = true;
-          commit<CG>(on, empty0 + 8 * stage);   // the stage is free once these MMAs have read it
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        commit<CG>(on, accfull0 + 8 * buf);
+        if (elect()) commit<CG>(accfull0 + 8 * buf);
         if (++buf == C::NBUF) {
           buf = 0;
           acc_phase ^= 1u;
@@ -795,47 +781,11 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
       }
       if (any) {
         // every MMA this thread issued has completed before TMEM is released
-        commit_local<CG>(on, drained);
-        if (on) mbar_drain(drained, 0);
-      }
-    }
-  } else if (C::FP4 && CG == 2 && warp == C::SCALE_WARP) {
-    // ---------------- scale copies, ahead of the MMAs (the pair's first CTA)
-    if constexpr (C::FP4 && CG == 2) {
-      if (rank == 0) {
-        const uint32_t on = lane == 0;
-        int stage = 0;
-        uint32_t phase = 0;
-        bool ok = true, any = false;
-        for (int t = unit0; t < p.num_tiles && ok; t += units) {
-          for (int kb = kb0; kb < kb1; ++kb) {
-            // the buffer's last MMAs are done: the producer waited for them before it filled the stage again
-            ok = warp_wait(full0 + 8 * stage, phase, abort_flag, p.info, 14, p.wait_ns);
-            if (!ok) break;
-            fence_after();
-            const uint32_t sf = ring + stage * stage_bytes + C::B_BYTES;
-            const uint32_t ca = sf0 + stage * C::SF_COLS, cb = ca + 4 * C::ATOMS;
-#pragma unroll
-            for (int q = 0; q < C::ATOMS; ++q) {
-              copy_scales_pair(on, ca + 4 * q, smem_desc(sf + 512 * q, 128, 128, 0));
-#pragma unroll
-              for (int b = 0; b < C::SFB_TILES; ++b)   // one K tile's columns side by side
-                copy_scales_pair(on, cb + 4 * (C::SFB_TILES * q + b),
-                                 smem_desc(sf + C::SFA_BYTES + 512 * (C::ATOMS * b + q), 128, 128, 0));
-            }
-            commit_local<CG>(on, ready0 + 8 * stage);
-            any = true;
-            if (++stage == p.stages) {
-              stage = 0;
-              phase ^= 1u;
-            }
-          }
+        if (elect()) {
+          commit_local<CG>(drained);
+          mbar_drain(drained, 0);
         }
-        if (any) {
-          // every copy this thread issued has completed before TMEM is released
-          commit_local<CG>(on, drained + 8);
-          if (on) mbar_drain(drained + 8, 0);
-        }
+        __syncwarp();
       }
     }
   } else {
