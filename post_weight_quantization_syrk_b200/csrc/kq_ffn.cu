@@ -38,7 +38,7 @@ kq_status go(const char* what, const Maps& m, Params p, int problems, int ks, cu
   return launch<C>(what, m, p, st);
 }
 
-constexpr Cost kGated = {0.46, 0.38}, kStore = {0.36, 0.33};
+constexpr Cost kGated = {0.46, 0.38, 2.5, 0.5}, kStore = {0.36, 0.33, 2.5, 0.5};
 
 struct Shape {
   int64_t T, d, f;

@@ -54,7 +54,7 @@ kq_status run(const char* what, const kq_fp4* A, const kq_fp4* B0, const kq_fp4*
 template <int KIND, int EPI>
 kq_status choose(const char* what, const kq_fp4* A, const kq_fp4* B0, const kq_fp4* B1, const Params& p, cudaStream_t st) {
   constexpr bool MX = KIND == KIND_MX;
-  constexpr Cost cost = EPI == EPI_STORE ? Cost{0.6, MX ? 0.47 : 0.53} : Cost{0.7, MX ? 0.48 : 0.55};
+  constexpr Cost cost = EPI == EPI_STORE ? Cost{0.42, MX ? 0.36 : 0.38, 1.2, 1.2} : Cost{0.54, MX ? 0.35 : 0.37, 1.6, 1.6};
   const Plan plan = make_plan(p.M, kq::cdiv(p.M, 128) * kq::cdiv(p.N, Slim<KIND, EPI>::OUTC),
                               kq::cdiv(p.M, 256) * kq::cdiv(p.N, Pair<KIND, EPI>::OUTC), kq::cdiv(A->cols, 256), cost);
   if (plan.pair) return run<Pair<KIND, EPI>>(what, A, B0, B1, p, 1, st);

@@ -8,16 +8,14 @@
 // per row (64 bf16 or 256 codes, four MMA steps of 32 bytes) in the 128-byte
 // swizzle.  Scale bytes travel as whole 512-byte tiles (128 rows x 4 blocks) by
 // TMA to shared memory and from there to TMEM in one of two ways.  CG = 2: by
-// tcgen05.cp, issued by a warp of its own ahead of the MMAs.  (From the thread that
-// issues the MMAs the copies run in turn with them, about 53 cycles a tile, 6 tiles
-// with KQ_FP4_MX or 12 with KQ_FP4_NV beside the 512 MMA cycles of a stage: 0.60
-// and 0.83 us a stage, against 0.47 and 0.57 from another warp, at 8192 x 11008 x
-// 16384.)  CG = 1: two sets of four warps, taking stages in turn, a warp per lane
-// quarter, with tcgen05.st (the 16 bytes of a tile row are a lane's four columns,
-// of which an MMA of half a tile's rows needs two, so that TMEM holds a buffer per
-// stage for two CTAs).  Under the pair's dense stream of MMAs these stores wait for
-// TMEM (0.87 us a stage); in the 128-row tiles they beat the copies (16 x 4096 x
-// 11008 gated, NV: 20.4 us against 26.0).
+// tcgen05.cp, issued by the MMA thread ahead of the step that reads them (6 copies a
+// stage with KQ_FP4_MX, 12 with KQ_FP4_NV; 0.37 and 0.385 us a stage of 0.27 us of MMAs
+// at 8192 x 11008 x 16384.  From a warp of their own, which the MMA thread then waits
+// for: 0.42 and 0.45).  CG = 1: two sets of four warps, taking stages in turn, a warp
+// per lane quarter, with tcgen05.st (the 16 bytes of a tile row are a lane's four
+// columns, of which an MMA of half a tile's rows needs two, so that TMEM holds a buffer
+// per stage for two CTAs).  Under the pair's dense stream of MMAs these stores wait for
+// TMEM (0.87 us a stage).
 //
 // Shapes.  CG = 2: a CTA pair per 256 x 256 tile (cta_group::2), each CTA
 // holding 128 rows of A and of B, so an SM fetches 64 bytes per MMA cycle
@@ -33,9 +31,9 @@
 //
 // Warp roles: 0 TMA, 1 TMEM and MMA issue, 2-9 the epilogue (one lane per row, two
 // warps per lane quarter, output through a swizzled staging buffer so that rows
-// leave in full lines), 10 the scale copies of a pair.  With CG = 2 bf16 has two
-// accumulators used in turn; beside the scales only one fits, which the epilogue
-// takes into registers whole, so that the next tile's MMAs wait for that read only.
+// leave in full lines).  With CG = 2 bf16 has two accumulators used in turn; beside the
+// scales only one fits, which the epilogue takes into registers whole, so that the next
+// tile's MMAs wait for that read only (about 1.3 us a tile of 6 us at K = 4096).
 // Every mbarrier wait is bounded by a time limit; on expiry the kernel
 // records KQ_ERR_TIMEOUT, drains its copies (bounded), frees TMEM and returns.
 #pragma once
@@ -208,7 +206,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 // one).  The issuing warps run their loops as whole warps and branch on this around
 // a stage's instructions: the compiler then knows that one thread is left and
 // issues them back to back.  Instructions predicated on a lane number instead cost
-// some 80 cycles each (MX pairs, a stage of 10: 0.56 us, here 0.40).
+// some 80 cycles each (MX pairs, a stage of 4 MMAs and 6 copies: 0.56 us, here 0.37;
+// bf16 backward, 333 x 1001 x 2730, single CTAs: 43.4 us, here 41.4).
 __device__ __forceinline__ bool elect() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
@@ -1027,29 +1026,33 @@ struct Plan {
 
 // Microseconds a wave of tiles takes per stage of K, measured (B200, 1.9 GHz): 128-row
 // tiles and pairs.  Beside them a wave of 128-row tiles costs about 3 us and one of
-// pairs 2, a launch of pairs 4, and a split of K 2.5 + ks / 2.
+// pairs 2, a launch of pairs 4, and a split of K over ks CTAs `split` + `part` ks.
 struct Cost {
-  double slim, pair;
+  double slim, pair, split, part;
 };
 
 // M rows, `slim` and `pairs` tiles of either kind, `stages` of K.  Up to 64 rows the
 // product streams its weights: K is split until the CTAs, two to an SM, are about as
 // many as the SMs (11008 x 4096, 16 rows, MX: 9.9 us with 172 CTAs, 11.4 with 86, 15.4
-// with 344).  Above, the cheaper by the sums above (1024 x 4096 x 4096: 15.7 us on 64
-// pairs, 22.4 on 256 tiles; 512 rows: 14.8 on 32 pairs, 11.5 on 128 tiles; 333 x 1001 x
-// 5460: 16.4 us with K over 4 CTAs, 30.0 without).  Clusters are powers of two: of 5 or
-// 6 CTAs fewer fit the GPU at a time (64 x 4096 x 4096: 19.7 us over 5, 11.1 over 4).
+// with 344).  Above, the cheaper by the sums above (MX, 1024 x 4096 x 4096: 11.3 us on
+// 64 pairs, 18.7 on 256 tiles; 512 rows: 10.3 on 32 pairs, 9.8 on 128 tiles; gated, 333
+// x 1001 x 5460: 13.2 us with K over 2 CTAs, 13.9 without, 15.0 on 16 pairs; bf16 gated
+// 128 x 4096 x 11008: 50.6 on pairs, 59.3 on tiles).  Clusters are powers of two: of 5 or
+// 6 CTAs fewer fit the GPU at a time (64 x 4096 x 4096: 19.7 us over 5, 11.1 over 4), and
+// of 8 no more than a few (64 x 2048 x 5504, 128 CTAs: 17.5 us over 8, 8.5 over 4; 64 x
+// 512 x 11008, 32 CTAs: 9.6 over 8, 10.1 over 4).  A CTA is left four stages of K or more
+// (64 x 1024 x 4096, 16 stages: 8.8 us over 8, 7.5 over 4).
 inline Plan make_plan(int64_t M, int64_t slim, int64_t pairs, int64_t stages, Cost c) {
   constexpr int64_t kSms = 148, kPairs = 74;
   if (M <= 64) {
     int ks = 1;
-    while (ks < 8 && slim * ks * 2 <= 176 && ks * 2 <= stages) ks *= 2;
+    while (ks < 8 && slim * ks * 2 <= (ks < 4 ? 176 : 64) && ks * 8 <= stages) ks *= 2;
     return {false, ks};
   }
   Plan best = {true, 1};
   double t = 4 + (2 + c.pair * (double)stages) * (double)cdiv(pairs, kPairs);
-  for (int ks = 1; ks <= 8 && ks <= stages && (ks == 1 || slim * ks <= kSms); ks *= 2) {
-    const double u = (3 + c.slim * (double)cdiv(stages, ks)) * (double)cdiv(slim * ks, kSms) + (ks > 1 ? 2.5 + 0.5 * ks : 0);
+  for (int ks = 1; ks <= 8 && ks <= stages && (ks == 1 || slim * ks <= (ks < 8 ? kSms : 64)); ks *= 2) {
+    const double u = (3 + c.slim * (double)cdiv(stages, ks)) * (double)cdiv(slim * ks, kSms) + (ks > 1 ? c.split + c.part * ks : 0);
     if (u < t) {
       t = u;
       best = {false, ks};
