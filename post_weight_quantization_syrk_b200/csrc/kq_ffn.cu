@@ -9,6 +9,12 @@
 // H) in its epilogue; dX with K running over both weights; both weight gradients
 // in one grid.  dG and dU are rounded to bf16 once, as outputs, and the products
 // take those (each rounding 2^-9 relative at most, the level of dX's own).
+//
+// Measured at 4096 x 4096 x 11008: forward 491 to 551 us (1.34 to 1.50 PFLOP/s, with the
+// power limit; the tensor pipe is active 93 % of the cycles), backward 1.69 to 1.73 ms
+// (1.28 to 1.31).  333 x 1001 x 2730 backward: 41.4 us, its three dependent launches of
+// 12 to 15 us each bound by the length of a tile's chain of stages.  8 x 4096 x 11008
+// forward: 36 us, the weights at 5.0 TB/s.
 #include "kq_mma.cuh"
 
 namespace {

@@ -139,7 +139,10 @@ struct QuantParams {
 // columns of a row (ROW_LANES 32), or 128 of 4 rows (8) where rows are short,
 // two such pieces with their loads in flight together.  The grid covers the scale
 // tiles' padding (rows to 128, blocks to 4), whose bytes are zeros.  Bound by
-// memory: one read of M, one write of codes and scales (and of M_hat).
+// memory: one read of M, one write of codes and scales (and of M_hat).  4096 x 4096
+// fp32 to MX with M_hat: 24.1 us (5.9 TB/s, 91 % of a copy's rate); 2047 x 11008 bf16,
+// rows 8 elements apart, to NV with M_hat: 28.7 us (5.1 TB/s, 78 %, its divisions beside
+// the loads).
 template <typename T, int FMT, int ROW_LANES>
 __global__ void __launch_bounds__(256, 4) quantize_kernel(const QuantParams p) {
   constexpr int R = 2;                            // pieces of a warp
@@ -316,6 +319,12 @@ __global__ void __launch_bounds__(256, 4) quantize_kernel(const QuantParams p) {
 //    per CTA in shared memory, and K is split over a cluster of up to 8 CTAs, whose
 //    sums meet in distributed shared memory.
 // Sums are added in a fixed order in both.
+//
+// Measured: 4096 x 4096 MX, one bf16 vector 5.3 us; 11008 x 4096 10.7 us (24 MB, 2.2
+// TB/s), eight 12.9; 4096 x 11008 NV, eight fp32 vectors 22.6.  Bound by the
+// instructions that decode the codes (8 codes in some 20) and, with fp32 vectors, by the
+// three MMAs a step instead of one: half of the issue slots and a fifth of the DRAM
+// rate are in use at one vector.
 constexpr int kWarps = 8;
 constexpr int kDepth = 4;         // steps of codes in flight (a power of two)
 constexpr int kStageSteps = 12;   // steps of x parts in shared memory at a time (72 KB)

@@ -2,6 +2,13 @@
 // kq_fp4_gated_ffn: H = act(X Wg^T) * (X Wu^T) over such operands, on the
 // block-scaled tcgen05 kinds (see kq_mma.cuh).  Products and block scales are
 // applied in the tensor core, sums are fp32 in TMEM.
+//
+// Measured (2MNK flops): 8192 x 11008 x 4096 MX 144 us (5.1 PFLOP/s), NV 160; x 16384
+// 479 (6.2 PFLOP/s) and 511; gated 8192 x 4096 x 11008 MX 270, NV 290.  At long K a stage
+// takes 0.37 us of which the MMAs are 0.27 (ring of 5 stages, the loads' latency and the
+// copies of the scales); at K = 4096 a tile's read-out, which no MMA overlaps, adds a
+// fifth.  77 x 4096 x 4096 with the quantization of the 77 rows: 11.5 us; gated 16 x 4096
+// x 11008: 18.8 us, 2.7 TB/s of weights.
 #include "kq_fp4.cuh"
 #include "kq_mma.cuh"
 
