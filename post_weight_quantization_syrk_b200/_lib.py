@@ -571,7 +571,8 @@ def kq_solver_timing(enable):
 #
 # These calls take microseconds on the device, so their wrappers keep the host's
 # share small: integer device and stream handles instead of objects, one
-# allocation per result.
+# allocation per result.  What a call with a stream allocates belongs to that
+# stream: such a call makes it current and goes through itself.
 
 _DTYPES = {torch.float32: KQ_F32, torch.bfloat16: KQ_BF16}
 
@@ -588,9 +589,9 @@ def _device(first, *others):
     return dev
 
 
-def _handle(stream, dev):
-    """The CUDA stream handle as an integer: of `stream`, or the device's current one."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+def _handle(dev):
+    """The handle of the device's current stream as an integer."""
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _rows(t, dtype, name):
@@ -701,6 +702,9 @@ def kq_fp4_scale_bytes(rows: int, cols: int, format: int) -> int:
 def kq_fp4_quantize(M, format, gscale=None, M_hat=None, out=None, info=None, stream=None):
     """M (float32 or bf16 [rows, cols]) to a microscaled 4-bit matrix; M_hat
     float32 [rows, cols]: the values its codes stand for."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kq_fp4_quantize(M, format, gscale, M_hat, out, info)
     dtype = _dtype_code(M, "M")
     ldm = _rows(M, M.dtype, "M")
     rows, cols = M.shape
@@ -722,13 +726,16 @@ def kq_fp4_quantize(M, format, gscale=None, M_hat=None, out=None, info=None, str
         hat = M_hat.data_ptr()
     if info is None:
         info = new_info(M.device)
-    _check(load().kq_fp4_quantize(M.data_ptr(), dtype, ldm, out._ref, hat, ldh, info.data_ptr(), _handle(stream, dev)),
+    _check(load().kq_fp4_quantize(M.data_ptr(), dtype, ldm, out._ref, hat, ldh, info.data_ptr(), _handle(dev)),
            "kq_fp4_quantize")
     return out
 
 
 def kq_fp4_gemm(A, B, Y=None, dtype=torch.bfloat16, info=None, stream=None):
     """Y [A.rows, B.rows] = A B^T, bf16 or float32."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kq_fp4_gemm(A, B, Y, dtype, info)
     if Y is not None:
         dtype = Y.dtype
     code = _DTYPES.get(dtype)
@@ -738,13 +745,16 @@ def kq_fp4_gemm(A, B, Y=None, dtype=torch.bfloat16, info=None, stream=None):
     Y, ldy = _out(Y, A.rows, B.rows, dtype, A._like(), "Y", 8)
     if info is None:
         info = new_info(A.device)
-    _check(load().kq_fp4_gemm(A._ref, B._ref, Y.data_ptr(), code, ldy, info.data_ptr(), _handle(stream, dev)),
+    _check(load().kq_fp4_gemm(A._ref, B._ref, Y.data_ptr(), code, ldy, info.data_ptr(), _handle(dev)),
            "kq_fp4_gemm")
     return Y
 
 
 def kq_fp4_matvec(W, X, Y=None, stream=None):
     """Y [batch, W.rows] = X W^T for unquantized X [batch (1..8), W.cols], in X's dtype."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kq_fp4_matvec(W, X, Y)
     dtype = _dtype_code(X, "X")
     ldx = _rows(X, X.dtype, "X")
     dev = _device(X, W, Y)
@@ -752,19 +762,22 @@ def kq_fp4_matvec(W, X, Y=None, stream=None):
     if cols != W.cols:
         raise ValueError("X must be [batch, W.cols]")
     Y, ldy = _out(Y, batch, W.rows, X.dtype, X, "Y")
-    _check(load().kq_fp4_matvec(W._ref, X.data_ptr(), dtype, ldx, batch, Y.data_ptr(), ldy, _handle(stream, dev)),
+    _check(load().kq_fp4_matvec(W._ref, X.data_ptr(), dtype, ldx, batch, Y.data_ptr(), ldy, _handle(dev)),
            "kq_fp4_matvec")
     return Y
 
 
 def kq_fp4_gated_ffn(X, W_gate, W_up, act, H=None, info=None, stream=None):
     """H [X.rows, f] bf16 = act(X W_gate^T) * (X W_up^T) over 4-bit X and weights [f, d]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kq_fp4_gated_ffn(X, W_gate, W_up, act, H, info)
     dev = _device(X, W_gate, W_up, H, info)
     H, ldh = _out(H, X.rows, W_gate.rows, torch.bfloat16, X._like(), "H", 8)
     if info is None:
         info = new_info(X.device)
     _check(load().kq_fp4_gated_ffn(X._ref, W_gate._ref, W_up._ref, act, H.data_ptr(), ldh, info.data_ptr(),
-                                   _handle(stream, dev)), "kq_fp4_gated_ffn")
+                                   _handle(dev)), "kq_fp4_gated_ffn")
     return H
 
 
@@ -789,6 +802,9 @@ def _gated_weights(X, W_gate, W_up):
 
 def kq_gated_ffn(X, W_gate, W_up, act, H=None, info=None, stream=None):
     """H [tokens, f] = act(X W_gate^T) * (X W_up^T), all bf16."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kq_gated_ffn(X, W_gate, W_up, act, H, info)
     ldx, ldw = _tma_rows(X, "X"), _gated_weights(X, W_gate, W_up)
     dev = _device(X, W_gate, W_up, H, info)
     (tokens, d), f = X.shape, W_gate.shape[0]
@@ -796,7 +812,7 @@ def kq_gated_ffn(X, W_gate, W_up, act, H=None, info=None, stream=None):
     if info is None:
         info = new_info(X.device)
     _check(load().kq_gated_ffn(X.data_ptr(), tokens, d, ldx, W_gate.data_ptr(), W_up.data_ptr(), f, ldw, act,
-                               H.data_ptr(), ldh, info.data_ptr(), _handle(stream, dev)), "kq_gated_ffn")
+                               H.data_ptr(), ldh, info.data_ptr(), _handle(dev)), "kq_gated_ffn")
     return H
 
 
@@ -804,6 +820,9 @@ def kq_gated_ffn_backward(X, W_gate, W_up, dH, act, dG=None, dU=None, H=None, dX
                           need_dX=True, need_dW=True, info=None, stream=None):
     """(dG, dU, dX, dW_gate, dW_up) of kq_gated_ffn, all bf16; H (when given)
     gets the block's output.  need_dX / need_dW False: None in those places."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kq_gated_ffn_backward(X, W_gate, W_up, dH, act, dG, dU, H, dX, dW_gate, dW_up, need_dX, need_dW, info)
     ldx, ldw = _tma_rows(X, "X"), _gated_weights(X, W_gate, W_up)
     lddh = _rows(dH, torch.bfloat16, "dH")
     dev = _device(X, W_gate, W_up, dH, dG, dU, H, dX, dW_gate, dW_up, info)
@@ -832,5 +851,5 @@ def kq_gated_ffn_backward(X, W_gate, W_up, dH, act, dG=None, dU=None, H=None, dX
         X.data_ptr(), tokens, d, ldx, W_gate.data_ptr(), W_up.data_ptr(), f, ldw, act, dH.data_ptr(), lddh,
         dG.data_ptr(), dU.data_ptr(), ldg, None if H is None else H.data_ptr(), ldh,
         dX.data_ptr() if need_dX else None, lddx, dW_gate.data_ptr() if need_dW else None,
-        dW_up.data_ptr() if need_dW else None, lddw, info.data_ptr(), _handle(stream, dev)), "kq_gated_ffn_backward")
+        dW_up.data_ptr() if need_dW else None, lddw, info.data_ptr(), _handle(dev)), "kq_gated_ffn_backward")
     return dG, dU, (dX if need_dX else None), (dW_gate if need_dW else None), (dW_up if need_dW else None)

@@ -630,10 +630,11 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
     return true;
   };
 
+  uint32_t issued = 0, issued_phase = 0;   // of the producer; bit s: stage s
   if (warp == 0) {
     // ---------------- TMA producer
     int stage = 0;
-    uint32_t phase = 0, issued_phase = 0, issued = 0;   // bit s: stage s
+    uint32_t phase = 0;
     bool ok = true;
     const uint32_t stage_tx = (uint32_t)(p.a_rows * 128 + C::B_BYTES + (CG == 2 ? C::SFA_BYTES + C::SFB_BYTES : 0)) * CG;
     for (int t = unit0; t < p.num_tiles && ok; t += units) {
@@ -642,10 +643,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
       tile_coords(p, t - problem * p.problem_tiles, &tm, &tn);
       const int m0 = tm * 128 * CG + (int)rank * 128, n0 = tn * C::OUTC;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!warp_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.info, 11, p.wait_ns)) {
-          ok = false;
-          break;
-        }
+        ok = warp_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.info, 11, p.wait_ns);
+        if (!ok) break;
         if (elect()) {
           uint32_t fb = full0 + 8 * stage;
           if (rank == 0) mbar_arrive_expect_tx(fb, stage_tx);
@@ -689,18 +688,6 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
         if (++stage == p.stages) {
           stage = 0;
           phase ^= 1u;
-        }
-      }
-    }
-    if (!ok) {
-      // the copies in flight land before the CTA (or pair) can exit
-      const unsigned long long t0 = globaltimer();
-      for (int s = 0; s < S; ++s) {
-        if (!(issued >> s & 1u)) continue;
-        const uint32_t ph = issued_phase >> s & 1u;
-        while (rank == 0 && !try_wait(full0 + 8 * s, ph) && globaltimer() - t0 < kTimeoutNs) {
-        }
-        while (C::FP4 && CG == 1 && !try_wait(landed0 + 8 * s, ph) && globaltimer() - t0 < kTimeoutNs) {
         }
       }
     }
@@ -959,6 +946,23 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
 
   fence_before();
   __syncthreads();
+  if (warp == 0 && *abort_flag) {
+    // A wait gave up, so that copies may be in flight that nobody waited for: they land
+    // before the CTA (or pair) exits.  The second CTA's signal the first's barriers; it
+    // gives those that the first did not expect 100 us.
+    const unsigned long long t0 = globaltimer();
+    for (int s = 0; s < S; ++s) {
+      if (!(issued >> s & 1u)) continue;
+      const uint32_t ph = issued_phase >> s & 1u;
+      while (rank == 0 && !try_wait(full0 + 8 * s, ph) && globaltimer() - t0 < kTimeoutNs) {
+      }
+      while (C::FP4 && CG == 1 && !try_wait(landed0 + 8 * s, ph) && globaltimer() - t0 < kTimeoutNs) {
+      }
+    }
+    while (rank == 1 && globaltimer() - t0 < 100000) {
+    }
+    __syncwarp();
+  }
   if constexpr (CG == 1) {
     if (p.via_smem) {
       // sum of the cluster's partials in rank order; the tile's pieces of 8 columns are dealt to its CTAs

@@ -220,10 +220,13 @@ class LayerQuantizer:
         """W' (after rotate()) on a microscaled 4-bit floating-point grid,
         rounded to nearest, and the Kronecker loss of that: the format of the
         tensor cores beside the integer settings of quantize_all()."""
+        if stream is not None:
+            with torch.cuda.stream(stream):    # what it allocates belongs to that stream
+                return self.quantize_fp4(format)
         g = global_scale(self.Wp) if format == K.KQ_FP4_NV else None
         res = Fp4Result(None, torch.empty_like(self.Wp), torch.zeros(1, dtype=torch.float64, device=self.device))
-        res.matrix = K.kq_fp4_quantize(self.Wp, format, g, M_hat=res.W_hat, info=self.info, stream=stream)
-        self.loss(res, stream)
+        res.matrix = K.kq_fp4_quantize(self.Wp, format, g, M_hat=res.W_hat, info=self.info)
+        self.loss(res)
         return res
 
     def check(self, where="kronq"):
@@ -261,15 +264,18 @@ class GatedCalibration:
 
     def add(self, X, W_gate, W_up, dH, n_total, act=K.KQ_ACT_SILU, need_dX=True, stream=None):
         """One batch of tokens; n_total: the tokens of all batches.  Returns dX (or None)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):    # what it allocates belongs to that stream
+                return self.add(X, W_gate, W_up, dH, n_total, act, need_dX)
         ld = -(-self.d_ff // 8) * 8
         H = torch.empty((X.shape[0], ld), dtype=torch.bfloat16, device=self.device)[:, :self.d_ff]
         dG, dU, dX, _, _ = K.kq_gated_ffn_backward(X, W_gate, W_up, dH, act, H=H, need_dX=need_dX, need_dW=False,
-                                                   info=self.info, stream=stream)
+                                                   info=self.info)
         need = max(K.kq_accum_cov_workspace_size(X.shape[0], d) for d in (self.d_model, self.d_ff))
         if need > self._ws.numel():
             self._ws = K.workspace(need, self.device)
         for A, C in ((X, self.H_X), (H, self.H_X_down), (dG, self.H_G_gate), (dU, self.H_G_up)):
-            K.kq_accum_cov(A, C, 1.0 / n_total, True, self._ws, self.info, stream)
+            K.kq_accum_cov(A, C, 1.0 / n_total, True, self._ws, self.info)
         return dX
 
     def check(self, where="gated calibration"):
