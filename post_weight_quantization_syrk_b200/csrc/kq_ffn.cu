@@ -15,6 +15,9 @@
 // (1.28 to 1.31).  333 x 1001 x 2730 backward: 41.4 us, its three dependent launches of
 // 12 to 15 us each bound by the length of a tile's chain of stages.  8 x 4096 x 11008
 // forward: 36 us, the weights at 5.0 TB/s.
+#include <algorithm>
+#include <initializer_list>
+
 #include "kq_mma.cuh"
 
 namespace {
@@ -84,6 +87,17 @@ kq_status check(const char* what, const Shape& s, const uint16_t* X, int64_t ldx
   return KQ_OK;
 }
 
+// Outputs at the address of an input or of another output (views side by side in one
+// tensor are fine).
+kq_status distinct(const char* what, std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    if (!*o) continue;
+    if (std::find(o + 1, outs.end(), *o) != outs.end() || std::find(ins.begin(), ins.end(), *o) != ins.end())
+      return kq::fail(KQ_ERR_INVALID_ARG, "%s: an output is another tensor of the call", what);
+  }
+  return KQ_OK;
+}
+
 }  // namespace
 
 extern "C" kq_status kq_gated_ffn(const uint16_t* X, int64_t tokens, int64_t d, int64_t ldx, const uint16_t* W_gate,
@@ -99,6 +113,7 @@ extern "C" kq_status kq_gated_ffn(const uint16_t* X, int64_t tokens, int64_t d, 
   if (!H) return kq::fail(KQ_ERR_INVALID_ARG, "%s: NULL pointer", what);
   if (ldh < f) return kq::fail(KQ_ERR_INVALID_ARG, "%s: leading dimension too small", what);
   if (!kq::aligned(H, 2)) return kq::fail(KQ_ERR_ALIGNMENT, "%s: H aligned to its elements", what);
+  KQ_TRY(distinct(what, {H}, {X, W_gate, W_up}));
   Params p = {};
   p.act = act;
   p.out[0] = H;
@@ -134,6 +149,7 @@ extern "C" kq_status kq_gated_ffn_backward(const uint16_t* X, int64_t tokens, in
     return kq::fail(KQ_ERR_ALIGNMENT, "%s: tensors aligned to their elements", what);
   if (2 * kq::cdiv(f, 128) * kq::cdiv(d, 128) > (1 << 24))
     return kq::fail(KQ_ERR_UNSUPPORTED_SHAPE, "%s: more than 2^24 tiles of 128 x 128", what);
+  if (tokens > 0) KQ_TRY(distinct(what, {dG, dU, H, dX, dW_gate, dW_up}, {X, W_gate, W_up, dH}));
   cudaStream_t st = (cudaStream_t)stream;
   if (tokens == 0) {
     for (uint16_t* w : {dW_gate, dW_up})

@@ -690,6 +690,7 @@ extern "C" kq_status kq_fp4_quantize(const void* M, int dtype, int64_t ldm, cons
   if (ldm < Q->cols || (M_hat && ldh < Q->cols)) return kq::fail(KQ_ERR_INVALID_ARG, "kq_fp4_quantize: leading dimension too small");
   if (!kq::aligned(M, esize) || (M_hat && !kq::aligned(M_hat, 4)))
     return kq::fail(KQ_ERR_ALIGNMENT, "kq_fp4_quantize: M and M_hat aligned to their elements");
+  if (M_hat == M) return kq::fail(KQ_ERR_INVALID_ARG, "kq_fp4_quantize: M_hat must not overlap M");
   QuantParams p = {};
   p.rows = Q->rows;
   p.cols = (int)Q->cols;
