@@ -3,11 +3,11 @@
 // block-scaled tcgen05 kinds (see kq_mma.cuh).  Products and block scales are
 // applied in the tensor core, sums are fp32 in TMEM.
 //
-// Measured (2MNK flops): 8192 x 11008 x 4096 MX 144 us (5.1 PFLOP/s), NV 160; x 16384
-// 479 (6.2 PFLOP/s) and 511; gated 8192 x 4096 x 11008 MX 270, NV 290.  At long K a stage
-// takes 0.37 us of which the MMAs are 0.27 (ring of 5 stages, the loads' latency and the
-// copies of the scales); at K = 4096 a tile's read-out, which no MMA overlaps, adds a
-// fifth.  77 x 4096 x 4096 with the quantization of the 77 rows: 11.5 us; gated 16 x 4096
+// Measured (2MNK flops): 8192 x 11008 x 4096 MX 134 to 139 us (5.5 to 5.3
+// PFLOP/s), NV 143 to 148; x 16384 467 to 486 (6.3 to 6.1 PFLOP/s) and 506 to 520; gated
+// 8192 x 4096 x 11008 MX 261, NV 281.  At long K a stage takes 0.37 us of which the MMAs
+// are 0.27 (ring of 5 stages, the loads' latency and the copies of the scales; with 4
+// stages 0.39); at K = 4096 a tile's read-out, which no MMA overlaps, adds an eighth.  77 x 4096 x 4096 with the quantization of the 77 rows: 11.5 us; gated 16 x 4096
 // x 11008: 18.8 us, 2.7 TB/s of weights.
 #include "kq_fp4.cuh"
 #include "kq_mma.cuh"

@@ -33,7 +33,7 @@
 // warps per lane quarter, output through a swizzled staging buffer so that rows
 // leave in full lines).  With CG = 2 bf16 has two accumulators used in turn; beside the
 // scales only one fits, which the epilogue takes into registers whole, so that the next
-// tile's MMAs wait for that read only (about 1.3 us a tile of 6 us at K = 4096).
+// tile's MMAs wait for that read only (about 0.9 us a tile of 7 us at K = 4096).
 // Every mbarrier wait is bounded by a time limit; on expiry the kernel
 // records KQ_ERR_TIMEOUT, drains its copies (bounded), frees TMEM and returns.
 #pragma once
