@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 4 ? 3 : 4) matvec_ke
 
 #pragma unroll
   for (int n = 0; n < kDepth - 1; ++n) fetch(n);
-  int staged = 0;   // steps below this one are in shared memory
+  int piece0 = 0, staged = 0;   // the parts of steps piece0 .. staged - 1 are in shared memory
   if (STAGED) {
     // vectors past the batch: zeros, written once
     for (int i = threadIdx.x; i < min(last - first, kStageSteps) * PARTS * 128; i += kWarps * 32)
@@ -517,6 +517,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 4 ? 3 : 4) matvec_ke
         }
       }
       __syncthreads();
+      piece0 = step;
       staged += n;
     }
     uint32_t xw[STAGED ? 1 : 16];
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 4 ? 3 : 4) matvec_ke
     for (int c = 0; c < PARTS; ++c)
 #pragma unroll
       for (int i = 0; i < 4; ++i) chain[c][i] = 0.f;
-    const uint4* xstep = xs + (STAGED ? (step - staged + min(kStageSteps, staged - first)) : 0) * PARTS * 128 + lane * 4;
+    const uint4* xstep = xs + (STAGED ? step - piece0 : 0) * PARTS * 128 + lane * 4;
     auto products = [&](bool sm) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
