@@ -11,11 +11,11 @@
 // tcgen05.cp, issued by the MMA thread ahead of the step that reads them (6 copies a
 // stage with KQ_FP4_MX, 12 with KQ_FP4_NV; 0.37 and 0.385 us a stage of 0.27 us of MMAs
 // at 8192 x 11008 x 16384.  From a warp of their own, which the MMA thread then waits
-// for: 0.42 and 0.45).  CG = 1: two sets of four warps, taking stages in turn, a warp
-// per lane quarter, with tcgen05.st (the 16 bytes of a tile row are a lane's four
-// columns, of which an MMA of half a tile's rows needs two, so that TMEM holds a buffer
-// per stage for two CTAs).  Under the pair's dense stream of MMAs these stores wait for
-// TMEM (0.87 us a stage).
+// for: 0.42 and 0.45).  CG = 1: two sets of four warps, one for the ring's even slots and
+// one for its odd ones, a warp per lane quarter, with tcgen05.st (the 16 bytes of a tile
+// row are a lane's four columns, of which an MMA of half a tile's rows needs two, so that
+// TMEM holds a buffer per stage for two CTAs).  Under the pair's dense stream of MMAs
+// these stores wait for TMEM (0.87 us a stage).
 //
 // Shapes.  CG = 2: a CTA pair per 256 x 256 tile (cta_group::2), each CTA
 // holding 128 rows of A and of B, so an SM fetches 64 bytes per MMA cycle
@@ -615,19 +615,28 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
   pdl_trigger();
   const uint32_t sf0 = tmem + C::NBUF * C::BN;
 
-  // CG = 1: the scales of this CTA's stages, every second one, by one warp of a set.
+  // CG = 1: the scales of this CTA's stages, by one warp of a set.  A set owns the slots of
+  // its parity, so that it waits for every phase of each: a parity wait on a phase whose
+  // predecessor another set saw passes too early while that one is still open.
   auto write_scales = [&](int set, int tn) {
-    for (int i = set; i < kb1 - kb0; i += 2) {
-      const uint32_t stage = (uint32_t)i % p.stages;
-      if (!warp_wait(landed0 + 8 * stage, ((uint32_t)i / p.stages) & 1u, abort_flag, p.info, 14, p.wait_ns)) return false;
-      // the slot's last MMAs are done: the producer waited for them before this stage's copies
-      fence_after();
-      if constexpr (C::FP4)
-        scales_to_tmem<C>(ring + stage * stage_bytes + C::B_BYTES,
-                          sf0 + stage * C::SF_COLS + ((uint32_t)(32 * (warp & 3)) << 16), tn & 1);
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ready0 + 8 * stage);
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int i = kb0; i < kb1; ++i) {
+      if ((slot & 1) == set) {
+        if (!warp_wait(landed0 + 8 * slot, phase, abort_flag, p.info, 14, p.wait_ns)) return false;
+        // the slot's last MMAs are done: the producer waited for them before this stage's copies
+        fence_after();
+        if constexpr (C::FP4)
+          scales_to_tmem<C>(ring + slot * stage_bytes + C::B_BYTES,
+                            sf0 + slot * C::SF_COLS + ((uint32_t)(32 * (warp & 3)) << 16), tn & 1);
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ready0 + 8 * slot);
+      }
+      if (++slot == p.stages) {
+        slot = 0;
+        phase ^= 1u;
+      }
     }
     return true;
   };
