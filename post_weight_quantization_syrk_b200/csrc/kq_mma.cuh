@@ -35,7 +35,7 @@
 // scales only one fits, which the epilogue takes into registers whole, so that the next
 // tile's MMAs wait for that read only (about 0.9 us a tile of 7 us at K = 4096).
 // Every mbarrier wait is bounded by a time limit; on expiry the kernel
-// records KQ_ERR_TIMEOUT, drains its copies (bounded), frees TMEM and returns.
+// records KQ_ERR_TIMEOUT, lets its copies land (bounded), frees TMEM and returns.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -145,6 +145,13 @@ __device__ __forceinline__ void cluster_sync() {
 // cluster scope would wait for the warp's global stores too, some 1000 cycles.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Counts bytes that no copy will bring as arrived.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
   float4 v;
@@ -576,6 +583,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
   // [4S + 4]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * S + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* mate = tmem_slot + 2;   // CG = 2: the other CTA's issued stages, and whether it gave up
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S, landed0 = full0 + 16 * S, ready0 = full0 + 24 * S;
   const uint32_t accfull0 = full0 + 32 * S, accempty0 = accfull0 + 16, drained = accfull0 + 32;
   const uint32_t ring = full0 + C::BARS;
@@ -641,13 +649,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
     return true;
   };
 
-  uint32_t issued = 0, issued_phase = 0;   // of the producer; bit s: stage s
+  uint32_t issued = 0;   // stages whose copies the producer has issued
+  constexpr uint32_t cta_tx_fixed = C::B_BYTES + (CG == 2 ? C::SFA_BYTES + C::SFB_BYTES : 0);
+  const uint32_t cta_tx = (uint32_t)p.a_rows * 128 + cta_tx_fixed;   // bytes of a stage that a CTA brings
   if (warp == 0) {
     // ---------------- TMA producer
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    const uint32_t stage_tx = (uint32_t)(p.a_rows * 128 + C::B_BYTES + (CG == 2 ? C::SFA_BYTES + C::SFB_BYTES : 0)) * CG;
     for (int t = unit0; t < p.num_tiles && ok; t += units) {
       const int problem = t / p.problem_tiles;
       int tm, tn;
@@ -658,7 +667,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
         if (!ok) break;
         if (elect()) {
           uint32_t fb = full0 + 8 * stage;
-          if (rank == 0) mbar_arrive_expect_tx(fb, stage_tx);
+          if (rank == 0) mbar_arrive_expect_tx(fb, cta_tx * CG);
           if (CG == 2) fb = mapa(fb, 0);
           const uint32_t sb = ring + stage * stage_bytes, sa = sb + C::A_OFF;
           const int seg = kb >= p.seg_blocks, k = kb - (seg ? p.seg_blocks : 0);
@@ -694,14 +703,16 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
           }
         }
         __syncwarp();
-        issued |= 1u << stage;
-        issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+        ++issued;
         if (++stage == p.stages) {
           stage = 0;
           phase ^= 1u;
         }
       }
     }
+    // the arrivals that free the last stages land before the CTA exits
+    for (uint32_t i = issued - min(issued, (uint32_t)p.stages); i < issued && ok; ++i)
+      ok = warp_wait(empty0 + 8 * (i % p.stages), i / p.stages & 1u, abort_flag, p.info, 17, p.wait_ns);
   } else if (warp == 1) {
     // ---------------- MMA issuer (the pair's first CTA)
     if (rank == 0) {
@@ -957,22 +968,39 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
 
   fence_before();
   __syncthreads();
-  if (warp == 0 && *abort_flag) {
+  bool expired = *abort_flag;
+  uint32_t mate_issued = issued;
+  if constexpr (CG == 2) {
+    if (threadIdx.x == 0) st_cluster(mapa(smem_u32(const_cast<uint32_t*>(mate)), rank ^ 1u), issued << 1 | (expired ? 1u : 0u));
+    cluster_sync();                                // both CTAs are done with each other's memory
+    const uint32_t word = *mate;
+    expired |= word & 1u;
+    mate_issued = word >> 1;
+  }
+  if (expired) {
     // A wait gave up, so that copies may be in flight that nobody waited for: they land
-    // before the CTA (or pair) exits.  The second CTA's signal the first's barriers; it
-    // gives those that the first did not expect 100 us.
-    const unsigned long long t0 = globaltimer();
-    for (int s = 0; s < S; ++s) {
-      if (!(issued >> s & 1u)) continue;
-      const uint32_t ph = issued_phase >> s & 1u;
-      while (rank == 0 && !try_wait(full0 + 8 * s, ph) && globaltimer() - t0 < kTimeoutNs) {
+    // before the CTA (or pair) exits.  The pair's copies all signal the first CTA's
+    // barriers, which expect both halves of a stage once that CTA has issued its own; the
+    // two may have stopped up to a ring apart.  So the first CTA takes the halves that the
+    // second never issued as arrived, announces those that it did not expect, and waits.
+    if (warp == 0 && rank == 0) {
+      if (CG == 2 && elect()) {
+        for (uint32_t i = mate_issued; i < issued; ++i) mbar_complete_tx(full0 + 8 * (i % p.stages), cta_tx);
+        for (uint32_t i = issued; i < mate_issued; ++i) mbar_arrive_expect_tx(full0 + 8 * (i % p.stages), cta_tx);
       }
-      while (C::FP4 && CG == 1 && !try_wait(landed0 + 8 * s, ph) && globaltimer() - t0 < kTimeoutNs) {
+      __syncwarp();
+      const unsigned long long t0 = globaltimer();
+      const uint32_t n = max(issued, mate_issued);
+      for (uint32_t i = n - min(n, (uint32_t)p.stages); i < n; ++i) {
+        const uint32_t slot = i % p.stages, ph = i / p.stages & 1u;
+        while (!try_wait(full0 + 8 * slot, ph) && globaltimer() - t0 < kTimeoutNs) {
+        }
+        while (C::FP4 && CG == 1 && !try_wait(landed0 + 8 * slot, ph) && globaltimer() - t0 < kTimeoutNs) {
+        }
       }
+      __syncwarp();
     }
-    while (rank == 1 && globaltimer() - t0 < 100000) {
-    }
-    __syncwarp();
+    if (CG == 2) cluster_sync();
   }
   if constexpr (CG == 1) {
     if (p.via_smem) {
@@ -1022,8 +1050,6 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
       }
       if (ks > 1) cluster_sync();                  // the partials stay until every CTA has read them
     }
-  } else {
-    cluster_sync();                                // both CTAs are done with each other's memory
   }
   if (warp == 1) {
     fence_after();
