@@ -260,10 +260,10 @@ class GatedCalibration:
         self.H_G_up = torch.zeros((d_ff, d_ff), **f32)
         self.d_model, self.d_ff, self.device = d_model, d_ff, dev
         self.info = K.new_info(dev)
-        self._ws = K.workspace(256, dev)
 
     def add(self, X, W_gate, W_up, dH, n_total, act=K.KQ_ACT_SILU, need_dX=True, stream=None):
-        """One batch of tokens; n_total: the tokens of all batches.  Returns dX (or None)."""
+        """One batch of tokens; n_total: the tokens of all batches.  Returns dX (or None).
+        Batches add to the same matrices: the caller orders those on different streams."""
         if stream is not None:
             with torch.cuda.stream(stream):    # what it allocates belongs to that stream
                 return self.add(X, W_gate, W_up, dH, n_total, act, need_dX)
@@ -271,11 +271,11 @@ class GatedCalibration:
         H = torch.empty((X.shape[0], ld), dtype=torch.bfloat16, device=self.device)[:, :self.d_ff]
         dG, dU, dX, _, _ = K.kq_gated_ffn_backward(X, W_gate, W_up, dH, act, H=H, need_dX=need_dX, need_dW=False,
                                                    info=self.info)
-        need = max(K.kq_accum_cov_workspace_size(X.shape[0], d) for d in (self.d_model, self.d_ff))
-        if need > self._ws.numel():
-            self._ws = K.workspace(need, self.device)
+        # of this call and its stream: a buffer kept between calls could be freed, when it
+        # grows, while another stream's kernels are still to use it
+        ws = K.workspace(max(K.kq_accum_cov_workspace_size(X.shape[0], d) for d in (self.d_model, self.d_ff)), self.device)
         for A, C in ((X, self.H_X), (H, self.H_X_down), (dG, self.H_G_gate), (dU, self.H_G_up)):
-            K.kq_accum_cov(A, C, 1.0 / n_total, True, self._ws, self.info)
+            K.kq_accum_cov(A, C, 1.0 / n_total, True, ws, self.info)
         return dX
 
     def check(self, where="gated calibration"):
