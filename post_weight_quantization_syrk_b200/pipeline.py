@@ -70,11 +70,15 @@ class LayerQuantizer:
             self.Hq = torch.empty((d_in, d_in), **f32)
             self.Wq = torch.empty((d_out, d_in), **f32)
 
-    def workspace(self, nbytes):
-        """One scratch buffer shared by the calls (they run in stream order)."""
+    def workspace(self, nbytes, stream=None):
+        """One scratch buffer shared by the calls (they run in stream order), for a
+        call on `stream` (None: the current one)."""
         if nbytes > self._ws_bytes:
             self._ws = K.workspace(nbytes, self.device)
             self._ws_bytes = nbytes
+        # the call may run on another stream than the one the buffer was allocated on: once
+        # a larger one replaces it, its memory waits for that stream too
+        self._ws.record_stream(torch.cuda.current_stream(self.device) if stream is None else stream)
         return self._ws
 
     def alloc_result(self, bits, group, solve_out=None):
@@ -110,7 +114,7 @@ class LayerQuantizer:
         n_total = X.shape[0] if n_total is None else n_total
         alpha = 1.0 / n_total if n_total else 0.0
         ws = self.workspace(max(K.kq_accum_cov_workspace_size(X.shape[0], self.d_in),
-                                K.kq_accum_cov_workspace_size(G.shape[0], self.d_out)))
+                                K.kq_accum_cov_workspace_size(G.shape[0], self.d_out)), stream)
         K.kq_accum_cov(X, self.H_X, alpha, accumulate, ws, self.info, stream)
         K.kq_accum_cov(G, self.H_G, alpha, accumulate, ws, self.info, stream)
 
@@ -150,7 +154,7 @@ class LayerQuantizer:
     def factor(self, damp_frac=0.01, stream=None):
         """Damped Cholesky factor of the inverse of H_X' (of the act-order
         permuted H_X' when act_order; dead flags then in that order)."""
-        ws = self.workspace(K.kq_chol_inv_workspace_size(self.d_in))
+        ws = self.workspace(K.kq_chol_inv_workspace_size(self.d_in), stream)
         H = self.H_X
         if self.act_order:
             K.kq_act_order_permutation(self.H_X, self.perm_in, stream)
@@ -173,7 +177,7 @@ class LayerQuantizer:
             K.kq_gather(r.W_hat_q, r.W_hat, None, self.inv_in, self.info, stream)
 
     def quantize(self, res: BitResult, stream=None):
-        ws = self.workspace(K.kq_quantize_layer_workspace_size(self.d_out, self.d_in, self.block))
+        ws = self.workspace(K.kq_quantize_layer_workspace_size(self.d_out, self.d_in, self.block), stream)
         Win = self._solve_input(stream)
         codes, W_hat = (res.codes_q, res.W_hat_q) if self.act_order else (res.codes, res.W_hat)
         K.kq_quantize_layer(Win, self.Uc, self.dead, res.bits, res.group, codes, res.scales, res.zeros,
@@ -181,14 +185,15 @@ class LayerQuantizer:
         self._unpermute(res, stream)
 
     def loss(self, res: BitResult, stream=None):
-        ws = self.workspace(K.kq_kron_loss_workspace_size(self.d_out, self.d_in))
+        ws = self.workspace(K.kq_kron_loss_workspace_size(self.d_out, self.d_in), stream)
         K.kq_kron_loss(self.Wp, res.W_hat, self.H_X, self.H_G, res.loss, ws, stream)
 
     def quantize_all(self, results, stream=None):
         """Every setting of `results` in one call: the factor's operand split is
         shared, and up to four settings are solved as one stacked problem
         (results from alloc_results) or else side by side."""
-        ws = self.workspace(K.kq_quantize_layer_multi_workspace_size(self.d_out, self.d_in, self.block, len(results)))
+        ws = self.workspace(K.kq_quantize_layer_multi_workspace_size(self.d_out, self.d_in, self.block, len(results)),
+                            stream)
         Win = self._solve_input(stream)
         q = self.act_order
         K.kq_quantize_layer_multi(Win, self.Uc, self.dead, [(r.bits, r.group) for r in results],
@@ -200,7 +205,7 @@ class LayerQuantizer:
 
     def loss_all(self, results, stream=None):
         """Every result's Kronecker loss in one call (the split of the smaller Hessian is shared)."""
-        ws = self.workspace(K.kq_kron_loss_workspace_size(self.d_out, self.d_in))
+        ws = self.workspace(K.kq_kron_loss_workspace_size(self.d_out, self.d_in), stream)
         K.kq_kron_loss_multi(self.Wp, [r.W_hat for r in results], self.H_X, self.H_G, [r.loss for r in results], ws,
                              stream)
 
@@ -355,7 +360,7 @@ class BlockwiseLayerQuantizer(LayerQuantizer):
         n_total = X.shape[0] if n_total is None else n_total
         alpha = 1.0 / n_total if n_total else 0.0
         ws = self.workspace(max(K.kq_accum_cov_workspace_size(X.shape[0], self.d_in),
-                                K.kq_accum_cov_blocks_workspace_size(G.shape[0], self.d_out, self.k)))
+                                K.kq_accum_cov_blocks_workspace_size(G.shape[0], self.d_out, self.k)), stream)
         K.kq_accum_cov(X, self.H_X, alpha, False, ws, self.info, stream)
         if self.balanced:
             K.kq_channel_energy(G, self.energy, alpha, None, self.info, stream)
@@ -388,7 +393,7 @@ class BlockwiseLayerQuantizer(LayerQuantizer):
             K.kq_rotate(Hb, K.KQ_AXIS_ROWS, T_k, False, stream)
 
     def loss(self, res: BitResult, stream=None):
-        ws = self.workspace(K.kq_kron_loss_blocks_workspace_size(self.d_out, self.d_in, self.k))
+        ws = self.workspace(K.kq_kron_loss_blocks_workspace_size(self.d_out, self.d_in, self.k), stream)
         K.kq_kron_loss_blocks(self.Wp, res.W_hat, self.H_X, self.H_Gb, res.loss, ws, stream)
 
     def loss_all(self, results, stream=None):

@@ -26,3 +26,62 @@ def test_gated_calibration_takes_a_workspace_per_batch(monkeypatch):
         assert all(ws.numel() >= K.kq_accum_cov_workspace_size(*shape) for shape, ws in calls)
     assert len({id(calls[0][1]) for calls in batches}) == 3
     assert not any(ws is v for _, ws in used for v in vars(cal).values())      # none is kept for the next call
+
+
+class Buffer:
+    """A workspace that notes the streams it is recorded on."""
+
+    def __init__(self, nbytes, device):
+        self.nbytes, self.streams = nbytes, []
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+
+def test_layer_workspace_is_recorded_on_every_stream_that_uses_it(monkeypatch):
+    d_out, d_in = 256, 512
+    current = ["default"]
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *exc):
+            current.pop()
+
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: current[-1])
+    monkeypatch.setattr(K, "workspace", Buffer)
+    seen = []                                       # (call, its workspace, the stream it runs on)
+
+    def spy(name, ws_at, stream_at):
+        def call(*args):
+            seen.append((name, args[ws_at], current[-1] if args[stream_at] is None else args[stream_at]))
+        monkeypatch.setattr(K, name, call)
+
+    spy("kq_accum_cov", 4, 6)
+    spy("kq_chol_inv", 4, 6)
+    spy("kq_quantize_layer", 11, 13)
+    spy("kq_quantize_layer_multi", 10, 12)
+    spy("kq_kron_loss", 5, 6)
+    spy("kq_kron_loss_multi", 5, 6)
+    monkeypatch.setattr(K, "kq_fp4_quantize", lambda *a, **kw: None)
+    lq = pipeline.LayerQuantizer(d_out, d_in, device="cpu")
+    X, G = (torch.zeros((4096, d), dtype=torch.bfloat16) for d in (d_in, d_out))
+    lq.statistics(X, G, stream="s1")
+    lq.factor(stream="s2")
+    lq.factor()
+    res = lq.alloc_results([(4, 0), (3, 0)])
+    lq.quantize(res[0], stream="s1")
+    lq.quantize_all(res, stream="s3")
+    lq.loss_all(res, stream="s2")
+    lq.loss(res[0])
+    lq.quantize_fp4(K.KQ_FP4_MX, stream="s4")
+    assert [n for n, _, _ in seen] == ["kq_accum_cov"] * 2 + ["kq_chol_inv"] * 2 + [
+        "kq_quantize_layer", "kq_quantize_layer_multi", "kq_kron_loss_multi", "kq_kron_loss", "kq_kron_loss"]
+    assert {s for _, _, s in seen} == {"default", "s1", "s2", "s3", "s4"}
+    for name, ws, stream in seen:
+        assert stream in ws.streams, (name, stream)
