@@ -43,7 +43,8 @@
  *   - Every device wait is bounded; on expiry the kernel records
  *     KQ_ERR_TIMEOUT in `info` and returns.
  *   - The library is stateless apart from a thread-local last-error string
- *     and is safe to call from several host threads.  No C++ exception
+ *     and the error word of kq_default_info, and is safe to call from several
+ *     host threads.  No C++ exception
  *     crosses this ABI.
  */
 #ifndef KRONQ_H
@@ -98,6 +99,12 @@ unsigned long long kq_launch_count(void);
  * the previous limit.  Default KQ_WAIT_LIMIT_DEFAULT_NS (4 s). */
 #define KQ_WAIT_LIMIT_DEFAULT_NS 4000000000ull
 unsigned long long kq_set_wait_limit_ns(unsigned long long ns);
+
+/* A word to pass as `info` where the caller has none: device memory of the
+ * library's own on the current device, zero until an error is recorded in it
+ * (and like any `info` never cleared by the library).  NULL without a usable
+ * device (see kq_last_error). */
+int32_t* kq_default_info(void);
 
 /* --------------------------------------------------------------------------
  * kq_accum_cov - covariance accumulation (steps a1/a2).

@@ -16,5 +16,5 @@ from ._lib import (  # noqa: F401
     kq_quantize_layer_multi_workspace_size, kq_quantize_layer_workspace_size, kq_rotate, kq_sensitivity,
     kq_status_string, kq_version, load, new_info, workspace,
     KQ_ACT_GELU, KQ_ACT_SILU, KQ_BF16, KQ_F32, KQ_FP4_MX, KQ_FP4_NV, Fp4Matrix, kq_fp4_gated_ffn, kq_fp4_gemm,
-    kq_fp4_matvec, kq_fp4_quantize, kq_fp4_scale_bytes, kq_gated_ffn, kq_gated_ffn_backward,
+    kq_fp4_matvec, kq_fp4_quantize, kq_fp4_scale_bytes, kq_gated_ffn, kq_gated_ffn_backward, default_info,
 )

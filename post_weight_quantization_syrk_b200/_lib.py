@@ -31,6 +31,7 @@ KQ_ACT_SILU, KQ_ACT_GELU = 0, 1
 # Every symbol the header declares.
 EXPORTS = (
     "kq_status_string", "kq_last_error", "kq_version", "kq_launch_count", "kq_set_wait_limit_ns",
+    "kq_default_info",
     "kq_accum_cov_workspace_size", "kq_accum_cov", "kq_accum_cov_blocks_workspace_size", "kq_accum_cov_blocks",
     "kq_channel_energy_workspace_size", "kq_channel_energy", "kq_balance_permutation", "kq_gather",
     "kq_act_order_permutation",
@@ -81,6 +82,7 @@ _SIGS = {
     "kq_version": (_i32, []),
     "kq_launch_count": (ctypes.c_ulonglong, []),
     "kq_set_wait_limit_ns": (ctypes.c_ulonglong, [ctypes.c_ulonglong]),
+    "kq_default_info": (_vp, []),
     "kq_accum_cov_workspace_size": (_sz, [_i64, _i64]),
     "kq_accum_cov": (_i32, [_vp, _i64, _i64, _i64, _vp, _i64, _f32, _i32, _vp, _sz, _vp, _vp]),
     "kq_sensitivity": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp]),
@@ -185,6 +187,32 @@ def workspace(nbytes: int, device) -> torch.Tensor:
 
 def new_info(device) -> torch.Tensor:
     return torch.zeros(1, dtype=torch.int32, device=device)
+
+
+class _DeviceWord:
+    """One int32 at a device address, for torch."""
+
+    def __init__(self, ptr):
+        self.__cuda_array_interface__ = {"shape": (1,), "typestr": "<i4", "data": (ptr, False), "version": 3}
+
+
+_default_infos = {}
+
+
+def default_info(device=None) -> torch.Tensor:
+    """The word in which calls without an `info` of their own record device
+    errors: the library's, one per device (default: the current one).  Look at it
+    with check_info(), zero_() it to start again."""
+    dev = None if device is None else torch.device(device).index
+    if dev is None:
+        dev = torch.cuda.current_device()
+    if dev not in _default_infos:
+        with torch.cuda.device(dev):
+            ptr = load().kq_default_info()
+            if not ptr:
+                _check(5, "kq_default_info")      # KQ_ERR_CUDA
+            _default_infos[dev] = torch.as_tensor(_DeviceWord(ptr), device=f"cuda:{dev}")
+    return _default_infos[dev]
 
 
 def check_info(info: torch.Tensor, where: str = "device"):
@@ -572,7 +600,8 @@ def kq_solver_timing(enable):
 # These calls take microseconds on the device, so their wrappers keep the host's
 # share small: integer device and stream handles instead of objects, one
 # allocation per result.  What a call with a stream allocates belongs to that
-# stream: such a call makes it current and goes through itself.
+# stream: such a call makes it current and goes through itself.  A call without an
+# `info` records device errors in default_info().
 
 _DTYPES = {torch.float32: KQ_F32, torch.bfloat16: KQ_BF16}
 
@@ -592,6 +621,17 @@ def _device(first, *others):
 def _handle(dev):
     """The handle of the device's current stream as an integer."""
     return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _info(info, dev):
+    """Address of the call's error word: `info`, or the device's default one."""
+    if info is None:
+        info = _default_infos.get(dev)
+        if info is None:
+            info = default_info(dev)
+    elif info.dtype != torch.int32 or info.numel() < 1:
+        raise TypeError("info must be an int32 device word (new_info)")
+    return info.data_ptr()
 
 
 def _rows(t, dtype, name):
@@ -724,9 +764,7 @@ def kq_fp4_quantize(M, format, gscale=None, M_hat=None, out=None, info=None, str
     if M_hat is not None:
         ldh = _out(M_hat, rows, cols, torch.float32, M, "M_hat")[1]
         hat = M_hat.data_ptr()
-    if info is None:
-        info = new_info(M.device)
-    _check(load().kq_fp4_quantize(M.data_ptr(), dtype, ldm, out._ref, hat, ldh, info.data_ptr(), _handle(dev)),
+    _check(load().kq_fp4_quantize(M.data_ptr(), dtype, ldm, out._ref, hat, ldh, _info(info, dev), _handle(dev)),
            "kq_fp4_quantize")
     return out
 
@@ -743,9 +781,7 @@ def kq_fp4_gemm(A, B, Y=None, dtype=torch.bfloat16, info=None, stream=None):
         raise TypeError("Y must be float32 or bfloat16")
     dev = _device(A, B, Y, info)
     Y, ldy = _out(Y, A.rows, B.rows, dtype, A._like(), "Y", 8)
-    if info is None:
-        info = new_info(A.device)
-    _check(load().kq_fp4_gemm(A._ref, B._ref, Y.data_ptr(), code, ldy, info.data_ptr(), _handle(dev)),
+    _check(load().kq_fp4_gemm(A._ref, B._ref, Y.data_ptr(), code, ldy, _info(info, dev), _handle(dev)),
            "kq_fp4_gemm")
     return Y
 
@@ -774,9 +810,7 @@ def kq_fp4_gated_ffn(X, W_gate, W_up, act, H=None, info=None, stream=None):
             return kq_fp4_gated_ffn(X, W_gate, W_up, act, H, info)
     dev = _device(X, W_gate, W_up, H, info)
     H, ldh = _out(H, X.rows, W_gate.rows, torch.bfloat16, X._like(), "H", 8)
-    if info is None:
-        info = new_info(X.device)
-    _check(load().kq_fp4_gated_ffn(X._ref, W_gate._ref, W_up._ref, act, H.data_ptr(), ldh, info.data_ptr(),
+    _check(load().kq_fp4_gated_ffn(X._ref, W_gate._ref, W_up._ref, act, H.data_ptr(), ldh, _info(info, dev),
                                    _handle(dev)), "kq_fp4_gated_ffn")
     return H
 
@@ -809,10 +843,8 @@ def kq_gated_ffn(X, W_gate, W_up, act, H=None, info=None, stream=None):
     dev = _device(X, W_gate, W_up, H, info)
     (tokens, d), f = X.shape, W_gate.shape[0]
     H, ldh = _out(H, tokens, f, torch.bfloat16, X, "H", 8)
-    if info is None:
-        info = new_info(X.device)
     _check(load().kq_gated_ffn(X.data_ptr(), tokens, d, ldx, W_gate.data_ptr(), W_up.data_ptr(), f, ldw, act,
-                               H.data_ptr(), ldh, info.data_ptr(), _handle(dev)), "kq_gated_ffn")
+                               H.data_ptr(), ldh, _info(info, dev), _handle(dev)), "kq_gated_ffn")
     return H
 
 
@@ -845,11 +877,9 @@ def kq_gated_ffn_backward(X, W_gate, W_up, dH, act, dG=None, dU=None, H=None, dX
         dW_up, ld2 = _out(dW_up, f, d, bf, X, "dW_up", 8)
         if ld2 != lddw:
             raise ValueError("dW_gate and dW_up need the same leading dimension")
-    if info is None:
-        info = new_info(X.device)
     _check(load().kq_gated_ffn_backward(
         X.data_ptr(), tokens, d, ldx, W_gate.data_ptr(), W_up.data_ptr(), f, ldw, act, dH.data_ptr(), lddh,
         dG.data_ptr(), dU.data_ptr(), ldg, None if H is None else H.data_ptr(), ldh,
         dX.data_ptr() if need_dX else None, lddx, dW_gate.data_ptr() if need_dW else None,
-        dW_up.data_ptr() if need_dW else None, lddw, info.data_ptr(), _handle(dev)), "kq_gated_ffn_backward")
+        dW_up.data_ptr() if need_dW else None, lddw, _info(info, dev), _handle(dev)), "kq_gated_ffn_backward")
     return dG, dU, (dX if need_dX else None), (dW_gate if need_dW else None), (dW_up if need_dW else None)
