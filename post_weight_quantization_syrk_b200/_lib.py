@@ -686,9 +686,8 @@ class Fp4Matrix:
         if scales.dtype != torch.uint8 or not scales.is_contiguous() or \
                 scales.numel() < kq_fp4_scale_bytes(rows, cols, format):
             raise ValueError("scales must be contiguous uint8 with kq_fp4_scale_bytes(rows, cols, format) elements")
-        for t in (scales, gscale):
-            if t is not None and t.device != codes.device:
-                raise ValueError("codes, scales and gscale must lie on one device")
+        if scales.device != codes.device:
+            raise ValueError("codes, scales and gscale must lie on one device")
         self._codes, self._scales = codes, scales
         self._set(rows, cols, format, ld, codes.data_ptr(), scales.data_ptr(), gscale, codes.get_device())
 
@@ -707,6 +706,8 @@ class Fp4Matrix:
     def _set(self, rows, cols, format, ld, codes, scales, gscale, dev):
         if gscale is not None and (gscale.dtype != torch.float32 or gscale.numel() != 1):
             raise TypeError("gscale must be one float32 element")
+        if gscale is not None and gscale.get_device() != dev:
+            raise ValueError("codes, scales and gscale must lie on one device")
         self.rows, self.cols, self.format, self.ld = rows, cols, format, ld
         self.gscale, self._dev = gscale, dev
         self.c = kq_fp4(rows, cols, ld, format, codes, scales, None if gscale is None else gscale.data_ptr())
