@@ -827,8 +827,10 @@ def _tma_rows(t, name):
 
 
 def _gated_weights(X, W_gate, W_up):
-    ldw = _tma_rows(W_gate, "W_gate")
-    if W_up.shape != W_gate.shape or _tma_rows(W_up, "W_up") != ldw:
+    ldw, ld2 = _tma_rows(W_gate, "W_gate"), _tma_rows(W_up, "W_up")
+    if W_gate.shape[0] <= 1:
+        ldw = ld2 = max(ldw, ld2)     # single rows: the distance to the next is not used
+    if W_up.shape != W_gate.shape or ld2 != ldw:
         raise ValueError("W_gate and W_up need the same shape and leading dimension")
     if W_gate.shape[1] != X.shape[1]:
         raise ValueError("X [tokens, d], weights [f, d]")
@@ -876,6 +878,8 @@ def kq_gated_ffn_backward(X, W_gate, W_up, dH, act, dG=None, dU=None, H=None, dX
     if need_dW:
         dW_gate, lddw = _out(dW_gate, f, d, bf, X, "dW_gate", 8)
         dW_up, ld2 = _out(dW_up, f, d, bf, X, "dW_up", 8)
+        if f <= 1:
+            lddw = ld2 = max(lddw, ld2)
         if ld2 != lddw:
             raise ValueError("dW_gate and dW_up need the same leading dimension")
     _check(load().kq_gated_ffn_backward(
