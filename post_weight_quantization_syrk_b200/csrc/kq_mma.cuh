@@ -306,26 +306,17 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
 // N words per lane to N TMEM columns of the warp's lane quarter.
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* v) {
-  if constexpr (N == 4)
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3])
-                 : "memory");
-  else if constexpr (N == 8)
+  static_assert(N == 8 || N == 16, "8 columns (MX) or 16 (NV)");
+  if constexpr (N == 8)
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
                  "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
-  else {
-    static_assert(N % 16 == 0, "4, 8 or a multiple of 16 columns");
-#pragma unroll
-    for (int i = 0; i < N; i += 16)
-      asm volatile(
-          "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-              taddr + i),
-          "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7]),
-          "r"(v[i + 8]), "r"(v[i + 9]), "r"(v[i + 10]), "r"(v[i + 11]), "r"(v[i + 12]), "r"(v[i + 13]), "r"(v[i + 14]),
-          "r"(v[i + 15])
-          : "memory");
-  }
+  else
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
 }
 
 // One 512-byte scale tile to 4 TMEM columns, repeated in the four lane quarters
@@ -634,7 +625,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
         if (!warp_wait(landed0 + 8 * slot, phase, abort_flag, p.info, 14, p.wait_ns)) return false;
         // the slot's last MMAs are done: the producer waited for them before this stage's copies
         fence_after();
-        if constexpr (C::FP4)
+        if constexpr (C::FP4 && CG == 1)
           scales_to_tmem<C>(ring + slot * stage_bytes + C::B_BYTES,
                             sf0 + slot * C::SF_COLS + ((uint32_t)(32 * (warp & 3)) << 16), tn & 1);
         fence_before();
