@@ -8,7 +8,7 @@
 // launches of the tile engine (kq_mma.cuh): the gated product with dG, dU (and
 // H) in its epilogue; dX with K running over both weights; both weight gradients
 // in one grid.  dG and dU are rounded to bf16 once, as outputs, and the products
-// take those (each rounding 2^-9 relative at most, the level of dX's own).
+// take those (each rounding 2^-8 relative at most, as dX's own).
 //
 // Measured at 4096 x 4096 x 11008: forward 491 to 551 us (1.34 to 1.50 PFLOP/s, with the
 // power limit; the tensor pipe is active 93 % of the cycles), backward 1.69 to 1.73 ms
@@ -136,8 +136,8 @@ extern "C" kq_status kq_gated_ffn_backward(const uint16_t* X, int64_t tokens, in
   KQ_TRY(check(what, s, X, ldx, W_gate, W_up, ldw, act, info));
   if (!dW_gate != !dW_up) return kq::fail(KQ_ERR_INVALID_ARG, "%s: dW_gate and dW_up go together", what);
   // The tensor core truncates as it accumulates, up to 2^-24 of the sum per MMA of 16
-  // terms: a sum over 2^18 terms (tokens; or 2 f for dX) loses at most 2^-10, half of
-  // what rounding it to bf16 may.
+  // terms: a sum over 2^18 terms (tokens; or 2 f for dX) loses at most 2^-10, a quarter
+  // of what rounding it to bf16 may.
   if (dW_gate && tokens > (1 << 18))
     return kq::fail(KQ_ERR_UNSUPPORTED_SHAPE, "%s: weights' gradients of more than 2^18 tokens (call it per batch and add)", what);
   if (tokens > 0 && (!dH || !dG || !dU)) return kq::fail(KQ_ERR_INVALID_ARG, "%s: NULL pointer", what);

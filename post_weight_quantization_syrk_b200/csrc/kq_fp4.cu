@@ -141,8 +141,9 @@ struct QuantParams {
 // tiles' padding (rows to 128, blocks to 4), whose bytes are zeros.  Bound by
 // memory: one read of M, one write of codes and scales (and of M_hat).  4096 x 4096
 // fp32 to MX with M_hat: 24.1 us (5.9 TB/s, 91 % of a copy's rate); 2047 x 11008 bf16,
-// rows 8 elements apart, to NV with M_hat: 28.7 us (5.1 TB/s, 78 %, its divisions beside
-// the loads).
+// rows 8 elements apart, to NV with M_hat: 28.7 us (5.1 TB/s, 78 %: a reciprocal per
+// block, a product and two FMAs per element and the conversions take 63 % of the issue
+// slots, and the loads' latency is a third of a warp's time).
 template <typename T, int FMT, int ROW_LANES>
 __global__ void __launch_bounds__(256, 4) quantize_kernel(const QuantParams p) {
   constexpr int R = 2;                            // pieces of a warp
@@ -321,10 +322,13 @@ __global__ void __launch_bounds__(256, 4) quantize_kernel(const QuantParams p) {
 // Sums are added in a fixed order in both.
 //
 // Measured: 4096 x 4096 MX, one bf16 vector 5.3 us; 11008 x 4096 10.7 us (24 MB, 2.2
-// TB/s), eight 12.9; 4096 x 11008 NV, eight fp32 vectors 22.6.  Bound by the
-// instructions that decode the codes (8 codes in some 20) and, with fp32 vectors, by the
-// three MMAs a step instead of one: half of the issue slots and a fifth of the DRAM
-// rate are in use at one vector.
+// TB/s), eight 12.9; 4096 x 11008 NV, eight fp32 vectors 22.6; 8192 x 28672 NV 144 (0.9
+// TB/s), with bf16 vectors 67.  Nothing is saturated.  One bf16 vector, 11008 x 4096: the
+// SMs have warps for 70 % of the time and issue in 68 % of that (decoding, 8 codes in some
+// 20 instructions, keeps the ALU pipe 63 % busy), DRAM runs at 21 %; a warp has four
+// steps, so the rest is the fill and drain of each CTA's ring.  fp32 vectors: 40 % of the
+// issue slots, two CTAs to an SM, waits at the barriers around the parts' forming; the
+// three MMAs a step use 15 % of the tensor pipe.
 constexpr int kWarps = 8;
 constexpr int kDepth = 4;         // steps of codes in flight (a power of two)
 constexpr int kStageSteps = 12;   // steps of x parts in shared memory at a time (72 KB)

@@ -3,12 +3,14 @@
 // block-scaled tcgen05 kinds (see kq_mma.cuh).  Products and block scales are
 // applied in the tensor core, sums are fp32 in TMEM.
 //
-// Measured (2MNK flops): 8192 x 11008 x 4096 MX 134 to 139 us (5.5 to 5.3
-// PFLOP/s), NV 143 to 148; x 16384 467 to 486 (6.3 to 6.1 PFLOP/s) and 506 to 520; gated
-// 8192 x 4096 x 11008 MX 261, NV 281.  At long K a stage takes 0.37 us of which the MMAs
+// Measured (2MNK flops): 8192 x 11008 x 4096 MX 134 us (5.5 PFLOP/s, tensor pipe 71 %
+// active), NV 143; x 16384 467 (6.3 PFLOP/s) and 506; gated 8192 x 4096 x 11008 MX 261, NV
+// 281.  Back to back on random data the power limit lowers the clock: up to 158, 168, 561,
+// 617, 317 and 331.  At long K a stage takes 0.37 us of which the MMAs
 // are 0.27 (ring of 5 stages, the loads' latency and the copies of the scales; with 4
-// stages 0.39); at K = 4096 a tile's read-out, which no MMA overlaps, adds an eighth.  77 x 4096 x 4096 with the quantization of the 77 rows: 11.5 us; gated 16 x 4096
-// x 11008: 18.8 us, 2.7 TB/s of weights.
+// stages 0.39); at K = 4096 a tile's read-out, which no MMA overlaps, adds an eighth.
+// 77 x 4096 x 4096 with the quantization of the 77 rows: 11.5 us; 8 x 11008 x 4096 MX 10.2;
+// gated 16 x 4096 x 11008: 18.8 us, 2.7 TB/s of weights.
 #include "kq_fp4.cuh"
 #include "kq_mma.cuh"
 
@@ -69,7 +71,7 @@ kq_status choose(const char* what, const kq_fp4* A, const kq_fp4* B0, const kq_f
 }
 
 // Longest K: the tensor core truncates as it accumulates, up to 2^-24 of the sum per
-// MMA of 64 columns, so that a longer chain would lose more than bf16 rounding does.
+// MMA of 64 columns: over 2^20 columns 2^-10, a quarter of what a rounding to bf16 may lose.
 constexpr int64_t kMaxCols = 1 << 20;
 
 }  // namespace

@@ -31,8 +31,8 @@
 //
 // Warp roles: 0 TMA, 1 TMEM and MMA issue, 2-9 the epilogue (one lane per row, two
 // warps per lane quarter, output through a swizzled staging buffer so that rows
-// leave in full lines).  With CG = 2 bf16 has two accumulators used in turn; beside the
-// scales only one fits, which the epilogue takes into registers whole, so that the next
+// leave in full lines).  With CG = 2 bf16 has two accumulators used in turn; beside a
+// scale buffer for every stage only one fits, which the epilogue takes into registers whole, so that the next
 // tile's MMAs wait for that read only (about 0.9 us a tile of 7 us at K = 4096).
 // Every mbarrier wait is bounded by a time limit; on expiry the kernel
 // records KQ_ERR_TIMEOUT, lets its copies land (bounded), frees TMEM and returns.
@@ -1066,7 +1066,7 @@ struct Cost {
 // M rows, `slim` and `pairs` tiles of either kind, `stages` of K.  Up to 64 rows the
 // product streams its weights: K is split until the CTAs, two to an SM, are about as
 // many as the SMs (11008 x 4096, 16 rows, MX: 9.9 us with 172 CTAs, 11.4 with 86, 15.4
-// with 344).  Above, the cheaper by the sums above (MX, 1024 x 4096 x 4096: 11.3 us on
+// with 344; the bound of 176 was not measured between those).  Above, the cheaper by the sums above (MX, 1024 x 4096 x 4096: 11.3 us on
 // 64 pairs, 18.7 on 256 tiles; 512 rows: 10.3 on 32 pairs, 9.8 on 128 tiles; gated, 333
 // x 1001 x 5460: 13.2 us with K over 2 CTAs, 13.9 without, 15.0 on 16 pairs; bf16 gated
 // 128 x 4096 x 11008: 50.6 on pairs, 59.3 on tiles).  Clusters are powers of two: of 5 or
