@@ -389,12 +389,14 @@ __device__ __forceinline__ uint32_t weight(uint32_t spread_pair, uint32_t scale,
   return mul_bf16x2(spread_pair, scale);
 }
 
-// 32 elements of a bf16 vector from column k as 16 words, zeros past d_in.
+// 32 elements of a bf16 vector from column k as 16 words, zeros past d_in.  Plain loads
+// here and below: the kernel ahead on the stream may still write x while this one is being
+// scheduled, which the read-only path does not allow for.
 __device__ __forceinline__ void load_x(const __nv_bfloat16* x, int64_t k, int64_t d_in, bool vec, uint32_t (&w)[16]) {
   if (vec && k + 32 <= d_in) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(x + k + 8 * i));
+      const uint4 q = *reinterpret_cast<const uint4*>(x + k + 8 * i);
       w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
     }
   } else {
@@ -496,8 +498,9 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 4 ? 3 : 4) matvec_ke
         if (p.x_vec && k + 32 <= p.d_in) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const float4 q = __ldg(reinterpret_cast<const float4*>(x + k + e));
-            v[e] = q.x; v[e + 1] = q.y; v[e + 2] = q.z; v[e + 3] = q.w;
+            asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(v[e]), "=f"(v[e + 1]), "=f"(v[e + 2]), "=f"(v[e + 3])
+                         : "l"(x + k + e));
           }
         } else {
 #pragma unroll
