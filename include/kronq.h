@@ -89,7 +89,8 @@ int kq_version(void);
 unsigned long long kq_launch_count(void);
 
 /* Time limit of the device waits in the tensor-core kernels (kq_accum_cov,
- * and the products inside kq_quantize_layer and kq_kron_loss): a pipeline
+ * the products inside kq_quantize_layer and kq_kron_loss, the 4-bit products
+ * and the gated block): a pipeline
  * wait that has not completed after `ns` nanoseconds gives up, the kernel
  * records KQ_ERR_TIMEOUT in `info` (index = the wait's site), lets its own
  * copies and products finish (with the fixed default bound), frees its
@@ -595,8 +596,8 @@ kq_status kq_fp4_gated_ffn(const kq_fp4* X, const kq_fp4* W_gate, const kq_fp4* 
  *   the pair dW_gate, dW_up may be NULL (not computed).
  *   X, weights, dG, dU: 16-byte aligned, leading dimensions % 8 == 0; the other
  *   tensors aligned to their elements.  No output may overlap an input or
- *   another output.  tokens == 0: the weights' gradients are zeros, the other
- *   tensors may be NULL.
+ *   another output.  tokens == 0: the weights' gradients are zeros; X, dH and
+ *   the other outputs may be NULL.
  * All bf16 as uint16_t bit patterns.  Limits: 0 <= tokens <= 2^24 (2^18 with
  * dW_gate, dW_up: add the gradients of several calls beyond), 1 <= d, f <= 2^17.
  * `info`: KQ_ERR_TIMEOUT.  NaN and Inf propagate.
