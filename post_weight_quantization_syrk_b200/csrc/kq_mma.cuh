@@ -32,8 +32,9 @@
 // Warp roles: 0 TMA, 1 TMEM and MMA issue, 2-9 the epilogue (one lane per row, two
 // warps per lane quarter, output through a swizzled staging buffer so that rows
 // leave in full lines).  With CG = 2 bf16 has two accumulators used in turn; beside a
-// scale buffer for every stage only one fits, which the epilogue takes into registers whole, so that the next
-// tile's MMAs wait for that read only (about 0.9 us a tile of 7 us at K = 4096).
+// scale buffer for every stage only one fits, which the epilogue takes into registers
+// whole, so that the next tile's MMAs wait for that read only (about 0.9 us a tile of
+// 7 us at K = 4096).
 // Every mbarrier wait is bounded by a time limit; on expiry the kernel
 // records KQ_ERR_TIMEOUT, lets its copies land (bounded), frees TMEM and returns.
 #pragma once
@@ -962,7 +963,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CG == 1 ? 2 : 1) tile_kernel(co
   bool expired = *abort_flag;
   uint32_t mate_issued = issued;
   if constexpr (CG == 2) {
-    if (threadIdx.x == 0) st_cluster(mapa(smem_u32(const_cast<uint32_t*>(mate)), rank ^ 1u), issued << 1 | (expired ? 1u : 0u));
+    if (threadIdx.x == 0)
+      st_cluster(mapa(smem_u32(const_cast<uint32_t*>(mate)), rank ^ 1u), issued << 1 | (expired ? 1u : 0u));
+    __syncwarp();
     cluster_sync();                                // both CTAs are done with each other's memory
     const uint32_t word = *mate;
     expired |= word & 1u;
